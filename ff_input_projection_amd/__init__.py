@@ -18,8 +18,8 @@ import os
 
 import torch
 
-__all__ = ["FusedProjection", "FusedProjError", "SplitRope", "load_library", "LIB_PATH", "EXPORTED_SYMBOLS", "Desc",
-           "SplitRopeDesc"]
+__all__ = ["FusedProjection", "FusedProjError", "SplitRope", "LayerNorm", "load_library", "LIB_PATH",
+           "EXPORTED_SYMBOLS", "LAYER_NORM_SYMBOLS", "Desc", "SplitRopeDesc", "LayerNormDesc"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libfused_proj.so")
@@ -29,6 +29,10 @@ EXPORTED_SYMBOLS = ["fused_proj_validate", "fused_proj_create", "fused_proj_run"
                     "fused_proj_backward", "fused_proj_backward_noalloc", "fused_proj_noalloc_scratch_bytes",
                     "split_rope_validate", "split_rope_create", "split_rope_run", "split_rope_destroy",
                     "fused_proj_mfma_ceiling"]
+
+# include/layer_norm.h
+LAYER_NORM_SYMBOLS = ["layer_norm_validate", "layer_norm_create", "layer_norm_run", "layer_norm_backward_workspace_size",
+                      "layer_norm_backward", "layer_norm_destroy"]
 
 OK, EINVAL, EUNSUPPORTED, EALIGN, EALIAS, EHIP, ESCRATCH = 0, -1, -2, -3, -4, -5, -6
 BF16, F32 = 0, 1
@@ -62,6 +66,16 @@ class SplitRopeDesc(ctypes.Structure):
         ("n_heads", ctypes.c_int64), ("n_kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
         ("qkv_order", ctypes.c_int32), ("rope", ctypes.c_int32), ("rope_dims", ctypes.c_int64),
         ("rope_base", ctypes.c_double), ("pos_offset", ctypes.c_int64), ("k_transposed", ctypes.c_int32),
+    ]
+
+
+class LayerNormDesc(ctypes.Structure):
+    """Mirror of ``layer_norm_desc``."""
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("x_layout", ctypes.c_int32), ("batch", ctypes.c_int64), ("channels", ctypes.c_int64),
+        ("n_spatial", ctypes.c_int32), ("spatial", ctypes.c_int64 * 3), ("x_stride_batch", ctypes.c_int64),
+        ("x_stride_channel", ctypes.c_int64), ("x_stride_spatial", ctypes.c_int64 * 3), ("has_bias", ctypes.c_int32),
+        ("eps", ctypes.c_double),
     ]
 
 
@@ -113,6 +127,18 @@ def load_library():
     lib.split_rope_run.restype = ctypes.c_int
     lib.split_rope_destroy.argtypes = [vp]
     lib.split_rope_destroy.restype = ctypes.c_int
+    lib.layer_norm_validate.argtypes = [ctypes.POINTER(LayerNormDesc)]
+    lib.layer_norm_validate.restype = ctypes.c_int
+    lib.layer_norm_create.argtypes = [ctypes.POINTER(LayerNormDesc), ctypes.POINTER(vp)]
+    lib.layer_norm_create.restype = ctypes.c_int
+    lib.layer_norm_run.argtypes = [vp] * 7
+    lib.layer_norm_run.restype = ctypes.c_int
+    lib.layer_norm_backward_workspace_size.argtypes = [vp, ctypes.POINTER(ctypes.c_size_t)]
+    lib.layer_norm_backward_workspace_size.restype = ctypes.c_int
+    lib.layer_norm_backward.argtypes = [vp] * 9 + [ctypes.c_size_t, vp]
+    lib.layer_norm_backward.restype = ctypes.c_int
+    lib.layer_norm_destroy.argtypes = [vp]
+    lib.layer_norm_destroy.restype = ctypes.c_int
     lib.fused_proj_mfma_ceiling.argtypes = [ctypes.c_int, ctypes.c_uint, vp, ctypes.c_size_t, vp,
                                             ctypes.POINTER(ctypes.c_double)]
     lib.fused_proj_mfma_ceiling.restype = ctypes.c_int
@@ -159,16 +185,7 @@ def mfma_ceiling_launch(iterations: int, sink: torch.Tensor, stream=None, seed: 
 _DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
 
 
-def make_desc(x_shape, x_strides, layout: str, dtype: torch.dtype, *, w_layout: str = "cf",
-              has_bias: bool = False, ff_dim: int = 0, ff_act: str = "none", n_heads: int = 0,
-              head_dim: int = 0, rope: bool = False, rope_base: float = 10000.0, pos_offset: int = 0,
-              n_kv_heads: int = 0, qkv_order: str = "contiguous", rope_dims: int = 0,
-              ff_layout: str = "tokens_last") -> Desc:
-    """Descriptor from an activation's shape and element strides.
-    layout "channels_first": x [b, c, spatial...] (1-3 spatial dims);
-    layout "tokens_last": x [b, s, c]."""
-    d = Desc()
-    d.dtype = _DTYPES[dtype]
+def _fill_activation(d, x_shape, x_strides, layout: str):
     if layout == "channels_first":
         d.x_layout = X_CHANNELS_FIRST
         sp, sps = x_shape[2:], x_strides[2:]
@@ -185,6 +202,19 @@ def make_desc(x_shape, x_strides, layout: str, dtype: torch.dtype, *, w_layout: 
     for i, (n, st) in enumerate(zip(sp, sps)):
         d.spatial[i] = n
         d.x_stride_spatial[i] = st
+
+
+def make_desc(x_shape, x_strides, layout: str, dtype: torch.dtype, *, w_layout: str = "cf",
+              has_bias: bool = False, ff_dim: int = 0, ff_act: str = "none", n_heads: int = 0,
+              head_dim: int = 0, rope: bool = False, rope_base: float = 10000.0, pos_offset: int = 0,
+              n_kv_heads: int = 0, qkv_order: str = "contiguous", rope_dims: int = 0,
+              ff_layout: str = "tokens_last") -> Desc:
+    """Descriptor from an activation's shape and element strides.
+    layout "channels_first": x [b, c, spatial...] (1-3 spatial dims);
+    layout "tokens_last": x [b, s, c]."""
+    d = Desc()
+    d.dtype = _DTYPES[dtype]
+    _fill_activation(d, x_shape, x_strides, layout)
     d.w_layout = {"cf": W_CF, "fc": W_FC}[w_layout]
     d.has_bias = int(bool(has_bias))
     d.ff_dim = ff_dim
@@ -464,3 +494,6 @@ class SplitRope:
             self.close()
         except Exception:
             pass
+
+
+from .layer_norm import LayerNorm, make_layer_norm_desc, validate_layer_norm  # noqa: E402

@@ -1,0 +1,865 @@
+// Layer norm over the channels of a channels-first or token-major activation, forward and
+// backward (gfx950; the formulas are in layer_norm.h).
+//
+// The op moves bytes: forward reads x and writes y, backward reads x and dy and writes dx,
+// with about 10 and 20 VALU operations a value where the memory rate allows 28 and 42. Each
+// tensor is touched once: a token's channels stay in registers (as stored, unpacked again
+// for each use) between the sums over them and the output that needs the sums.
+//
+// Token-major rows: TPR threads (a wave, or a workgroup of 256 or 1024) hold a row, NCH
+// 16-byte pieces each. Channels-first: a workgroup holds a strip of TL * V tokens with all
+// channels; TL neighbouring lanes read TL * 16 contiguous bytes of one channel.
+//
+// The variance is the mean square of x - mean, from the held values: no cancellation.
+// dgamma and dbeta: every thread keeps its channels' sums in fp32 over the rows or strips
+// that its workgroup takes in turn; the workgroup's sums go to the workspace and a second
+// kernel adds them in 64 bits, in a fixed order.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <new>
+
+#include "../../include/layer_norm.h"
+#include "fused_proj_kernels.h"
+#include "vector_io.h"
+
+namespace {
+
+using namespace fp::dev;
+
+struct NormArgs {
+    const void* x;
+    const void* gamma;
+    const void* beta;      // nullptr without a bias
+    const void* dy;        // backward
+    void* y;               // y, or dx
+    float* mean;           // [b*S]; forward: nullptr when not wanted
+    float* rstd;
+    float* partial;        // backward: [workgroups, 2, C]
+    int64_t x_sb, x_ss, x_sc;   // element strides of x
+    int32_t M, S, C;
+    int32_t strips;        // channels-first: strips of a slab
+    int32_t all_strips;    // and of all of them
+    float inv_c, eps;
+    fp::FastDivU31 div_s;  // token -> slab; channels-first: strip -> slab (by strips)
+};
+
+// ------------------------------------------------------------------ token-major rows
+// Sum over the TPR threads of a row, the same bits in each; `red` holds a value a wave.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+    v = wave_sum(v);
+    if constexpr (TPR > 64) {
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < TPR / 64; ++w) v += red[w];
+        __syncthreads();
+    }
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ const T* row_of(const NormArgs& a, int row) {
+    const int bi = (int)fp::fastdiv_u31((uint32_t)row, a.div_s);
+    return static_cast<const T*>(a.x) + (int64_t)bi * a.x_sb + (int64_t)(row - bi * a.S) * a.x_ss;
+}
+
+template <typename T, int NCH, int TPR, bool TAIL>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void layer_norm_rows_kernel(NormArgs a) {
+    constexpr int V = Piece<T>::V, BLOCK = TPR < 256 ? 256 : TPR, RPB = BLOCK / TPR;
+    __shared__ float red[TPR > 64 ? TPR / 64 : 1];
+    const int lane = threadIdx.x % TPR;
+    const T* gamma = static_cast<const T*>(a.gamma);
+    const T* beta = static_cast<const T*>(a.beta);
+    for (int row = blockIdx.x * RPB + threadIdx.x / TPR; row < a.M; row += gridDim.x * RPB) {
+        const T* x = row_of<T>(a, row);
+        u32x4 h[NCH];
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const int c = (i * TPR + lane) * V;
+            h[i] = u32x4{0, 0, 0, 0};
+            if (c < a.C) h[i] = load_piece<T, TAIL>(x + c, a.C - c);
+        }
+#pragma unroll
+        for (int i = 0; i < NCH; ++i)
+#pragma unroll
+            for (int e = 0; e < V; ++e) sum += Piece<T>::get(h[i], e);   // past C: zeros
+        const float mean = row_sum<TPR>(sum, red) * a.inv_c;
+        float sq = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const int n = a.C - (i * TPR + lane) * V;
+            unpack_again(h[i]);
+            if (n > 0) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float d = Piece<T>::get(h[i], e) - mean;
+                    if (!TAIL || e < n) sq = fmaf(d, d, sq);
+                }
+            }
+        }
+        const float rstd = 1.0f / sqrtf(row_sum<TPR>(sq, red) * a.inv_c + a.eps);
+        T* y = static_cast<T*>(a.y) + (int64_t)row * a.C;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const int c = (i * TPR + lane) * V, n = a.C - c;
+            unpack_again(h[i]);
+            if (n > 0) {
+                const u32x4 g = load_piece<T, TAIL>(gamma + c, n);
+                const u32x4 b = beta ? load_piece<T, TAIL>(beta + c, n) : u32x4{0, 0, 0, 0};
+                float o[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    o[e] = fmaf((Piece<T>::get(h[i], e) - mean) * rstd, Piece<T>::get(g, e), Piece<T>::get(b, e));
+                store_piece<T, TAIL>(y + c, o, n);
+            }
+        }
+        if (a.mean && lane == 0) {
+            a.mean[row] = mean;
+            a.rstd[row] = rstd;
+        }
+    }
+}
+
+template <typename T, int NCH, int TPR, bool TAIL>
+__global__ __launch_bounds__(TPR < 512 ? 512 : TPR) void layer_norm_rows_grad_kernel(NormArgs a) {
+    constexpr int V = Piece<T>::V, BLOCK = TPR < 512 ? 512 : TPR, RPB = BLOCK / TPR, WPR = TPR / 64;
+    __shared__ float red[BLOCK / 64 * 2];
+    __shared__ float both[RPB > 1 ? 2 * NCH * TPR * V : 1];
+    const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+    const T* gamma = static_cast<const T*>(a.gamma);
+    float dg[NCH][V], db[NCH][V];
+#pragma unroll
+    for (int i = 0; i < NCH; ++i)
+#pragma unroll
+        for (int e = 0; e < V; ++e) dg[i][e] = db[i][e] = 0.0f;
+    // every row slot of the workgroup takes the same number of turns, so that its barriers meet
+    for (int first = blockIdx.x * RPB; first < a.M; first += gridDim.x * RPB) {
+        const int row = first + sub;
+        const bool real = row < a.M;
+        const T* x = row_of<T>(a, real ? row : 0);
+        const T* dy = static_cast<const T*>(a.dy) + (int64_t)(real ? row : 0) * a.C;
+        const float mean = a.mean[real ? row : 0], rstd = a.rstd[real ? row : 0];
+        u32x4 hx[NCH], hd[NCH];
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const int c = (i * TPR + lane) * V, n = a.C - c;
+            hx[i] = hd[i] = u32x4{0, 0, 0, 0};
+            if (real && n > 0) {
+                hx[i] = load_piece<T, TAIL>(x + c, n);
+                hd[i] = load_piece<T, TAIL>(dy + c, n);
+            }
+        }
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const int c = (i * TPR + lane) * V, n = a.C - c;
+            if (real && n > 0) {
+                const u32x4 g = load_piece<T, TAIL>(gamma + c, n);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    if (!TAIL || e < n) {
+                        const float d = Piece<T>::get(hd[i], e), xh = (Piece<T>::get(hx[i], e) - mean) * rstd;
+                        const float gd = d * Piece<T>::get(g, e);
+                        s1 += gd;
+                        s2 = fmaf(gd, xh, s2);
+                        dg[i][e] = fmaf(d, xh, dg[i][e]);
+                        db[i][e] += d;
+                    }
+                }
+            }
+        }
+        s1 = wave_sum(s1);
+        s2 = wave_sum(s2);
+        if constexpr (TPR > 64) {
+            const int wave = threadIdx.x >> 6, row_wave = wave / WPR * WPR;
+            if ((threadIdx.x & 63) == 0) {
+                red[2 * wave] = s1;
+                red[2 * wave + 1] = s2;
+            }
+            __syncthreads();
+            s1 = s2 = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WPR; ++w) {
+                s1 += red[2 * (row_wave + w)];
+                s2 += red[2 * (row_wave + w) + 1];
+            }
+            __syncthreads();
+        }
+        s1 *= a.inv_c;
+        s2 *= a.inv_c;
+        T* dx = static_cast<T*>(a.y) + (int64_t)row * a.C;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const int c = (i * TPR + lane) * V, n = a.C - c;
+            unpack_again(hx[i]);
+            unpack_again(hd[i]);
+            if (real && n > 0) {
+                const u32x4 g = load_piece<T, TAIL>(gamma + c, n);
+                float o[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float xh = (Piece<T>::get(hx[i], e) - mean) * rstd;
+                    o[e] = rstd * (fmaf(Piece<T>::get(hd[i], e), Piece<T>::get(g, e), -s1) - xh * s2);
+                }
+                store_piece<T, TAIL>(dx + c, o, n);
+            }
+        }
+    }
+    // the workgroup's sums: its row slots add theirs in turn
+    float* out = a.partial + (int64_t)blockIdx.x * 2 * a.C;
+    if constexpr (RPB > 1) {
+        for (int r = 0; r < RPB; ++r) {
+            if (sub == r) {
+#pragma unroll
+                for (int i = 0; i < NCH; ++i)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const int at = (i * TPR + lane) * V + e;
+                        both[at] = r == 0 ? dg[i][e] : both[at] + dg[i][e];
+                        both[NCH * TPR * V + at] = r == 0 ? db[i][e] : both[NCH * TPR * V + at] + db[i][e];
+                    }
+            }
+            __syncthreads();
+        }
+        for (int c = threadIdx.x; c < a.C; c += BLOCK) {
+            out[c] = both[c];
+            out[a.C + c] = both[NCH * TPR * V + c];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NCH; ++i)
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const int c = (i * TPR + lane) * V + e;
+                if (c < a.C) {
+                    out[c] = dg[i][e];
+                    out[a.C + c] = db[i][e];
+                }
+            }
+    }
+}
+
+// ------------------------------------------------------------------ channels-first strips
+// A workgroup's strip is TL * V tokens of one slab. Thread (cr, tl) holds V tokens of the
+// channels cr, cr + R, cr + 2R, ... (R = threads / TL).
+//
+// Sum of f[e] over the lanes of a wave with the same tl (lane bits 3..5, and 2 where TL is
+// 4): each exchange halves the values a lane carries, so the sums of 8 values cost 4 + 2 + 1
+// exchanges instead of 24. The lane's remaining value is the sum for token `lane_token`.
+template <int TL, int V>
+__device__ __forceinline__ float strip_sum(const float (&f)[V]) {
+    float r;
+    if constexpr (V == 8) {
+        const float a0 = swap_sum32(f[0], f[4]), a1 = swap_sum32(f[1], f[5]);
+        const float a2 = swap_sum32(f[2], f[6]), a3 = swap_sum32(f[3], f[7]);
+        const float b0 = swap_sum16(a0, a2), b1 = swap_sum16(a1, a3);
+        const bool odd = threadIdx.x & 8;
+        r = (odd ? b1 : b0) + dpp<kRowRor8>(odd ? b0 : b1);
+    } else {
+        const float a0 = swap_sum32(f[0], f[2]), a1 = swap_sum32(f[1], f[3]);
+        r = swap_sum16(a0, a1);
+        r += dpp<kRowRor8>(r);
+    }
+    if constexpr (TL == 4) r += dpp<0x1B>(dpp<kHalfMirror>(r));   // lane ^ 7, then ^ 3: lane ^ 4
+    return r;
+}
+template <int TL, int V>
+__device__ __forceinline__ int lane_token() {
+    const int l = threadIdx.x & 63, b5 = l >> 5, b4 = (l >> 4) & 1, b3 = (l >> 3) & 1;
+    return (l & (TL - 1)) * V + (V == 8 ? b5 * 4 + b4 * 2 + b3 : b5 * 2 + b4);
+}
+
+// Sums of NS sets of per-token values over the whole workgroup: tot[set][token], the same
+// bits for every thread. `red`: [waves][NS][TL * V].
+template <int TL, int V, int NS, int NT>
+__device__ __forceinline__ void strip_total(const float (&f)[NS][V], float* red, float* tot) {
+    constexpr int TT = TL * V, W = NT / 64;
+    const int t = lane_token<TL, V>();
+#pragma unroll
+    for (int s = 0; s < NS; ++s) red[((threadIdx.x >> 6) * NS + s) * TT + t] = strip_sum<TL, V>(f[s]);
+    __syncthreads();
+    if (threadIdx.x < NS * TT) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) v += red[w * NS * TT + threadIdx.x];
+        tot[threadIdx.x] = v;
+    }
+    __syncthreads();
+}
+
+// NCH > 0: the strip is held in registers, NCH pieces a thread. NCH = 0 (more channels than
+// that): it is read again for each use, from the caches.
+template <typename T, int NCH, int TL, int NT, bool TAIL>
+__global__ __launch_bounds__(NT) void layer_norm_strips_kernel(NormArgs a) {
+    constexpr int V = Piece<T>::V, R = NT / TL, TT = TL * V, HOLD = NCH > 0 ? NCH : 1;
+    __shared__ float red[NT / 64 * TT];
+    __shared__ float tot[2][TT];
+    const int tl = threadIdx.x % TL, cr = threadIdx.x / TL;
+    const int bi = (int)fp::fastdiv_u31(blockIdx.x, a.div_s), t0 = (int)(blockIdx.x - (uint32_t)bi * a.strips) * TT + tl * V;
+    const int n = a.S - t0;
+    const int nch = NCH > 0 ? NCH : (a.C + R - 1) / R;
+    const T* x = static_cast<const T*>(a.x) + (int64_t)bi * a.x_sb + t0;
+    u32x4 h[HOLD];
+    const auto load = [&](int i) {
+        const int c = i * R + cr;
+        return c < a.C && n > 0 ? load_piece<T, TAIL>(x + (int64_t)c * a.x_sc, n) : u32x4{0, 0, 0, 0};
+    };
+    if constexpr (NCH > 0) {
+#pragma unroll
+        for (int i = 0; i < HOLD; ++i) h[i] = load(i);
+    }
+    const auto piece = [&](int i) {
+        if constexpr (NCH > 0) {
+            unpack_again(h[i]);
+            return h[i];
+        } else {
+            return load(i);
+        }
+    };
+    float f[1][V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[0][e] = 0.0f;
+#pragma unroll NCH > 0 ? NCH : 1
+    for (int i = 0; i < nch; ++i) {
+        const u32x4 p = piece(i);
+#pragma unroll
+        for (int e = 0; e < V; ++e) f[0][e] += Piece<T>::get(p, e);
+    }
+    strip_total<TL, V, 1, NT>(f, red, tot[0]);
+    float mean[V], rstd[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        mean[e] = tot[0][tl * V + e] * a.inv_c;
+        f[0][e] = 0.0f;
+    }
+#pragma unroll NCH > 0 ? NCH : 1
+    for (int i = 0; i < nch; ++i) {
+        if (i * R + cr < a.C) {
+            const u32x4 p = piece(i);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float d = Piece<T>::get(p, e) - mean[e];
+                f[0][e] = fmaf(d, d, f[0][e]);
+            }
+        }
+    }
+    strip_total<TL, V, 1, NT>(f, red, tot[1]);
+#pragma unroll
+    for (int e = 0; e < V; ++e) rstd[e] = 1.0f / sqrtf(tot[1][tl * V + e] * a.inv_c + a.eps);
+    T* y = static_cast<T*>(a.y) + (int64_t)bi * a.C * a.S + t0;
+#pragma unroll NCH > 0 ? NCH : 1
+    for (int i = 0; i < nch; ++i) {
+        const int c = i * R + cr;
+        if (c < a.C && n > 0) {
+            const u32x4 p = piece(i);
+            const float g = (float)static_cast<const T*>(a.gamma)[c];
+            const float b = a.beta ? (float)static_cast<const T*>(a.beta)[c] : 0.0f;
+            float o[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) o[e] = fmaf((Piece<T>::get(p, e) - mean[e]) * rstd[e], g, b);
+            store_piece<T, TAIL>(y + (int64_t)c * a.S, o, n);
+        }
+    }
+    if (a.mean && cr == 0) {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            if (e < n) {
+                a.mean[(int64_t)bi * a.S + t0 + e] = mean[e];
+                a.rstd[(int64_t)bi * a.S + t0 + e] = rstd[e];
+            }
+    }
+}
+
+// Sum over the TL token lanes of a channel, in each of them.
+template <int TL>
+__device__ __forceinline__ float token_sum(float v) {
+    v += dpp<kQuadXor1>(v);
+    v += dpp<kQuadXor2>(v);
+    if constexpr (TL == 8) v += dpp<kHalfMirror>(v);
+    return v;
+}
+
+template <typename T, int NCH, int TL, int NT, bool TAIL>
+__global__ __launch_bounds__(NT) void layer_norm_strips_grad_kernel(NormArgs a) {
+    constexpr int V = Piece<T>::V, R = NT / TL, TT = TL * V, HOLD = NCH > 0 ? NCH : 1;
+    __shared__ float red[NT / 64 * 2 * TT];
+    __shared__ float tot[2][TT];
+    const int tl = threadIdx.x % TL, cr = threadIdx.x / TL;
+    const int nch = NCH > 0 ? NCH : (a.C + R - 1) / R;
+    float* out = a.partial + (int64_t)blockIdx.x * 2 * a.C;
+    float dg[HOLD], db[HOLD];
+#pragma unroll
+    for (int i = 0; i < HOLD; ++i) dg[i] = db[i] = 0.0f;
+    bool first = true;
+    for (int strip = blockIdx.x; strip < a.all_strips; strip += gridDim.x) {
+        const int bi = (int)fp::fastdiv_u31((uint32_t)strip, a.div_s), t0 = (strip - bi * a.strips) * TT + tl * V;
+        const int n = a.S - t0;
+        const T* x = static_cast<const T*>(a.x) + (int64_t)bi * a.x_sb + t0;
+        const int64_t dense = (int64_t)bi * a.C * a.S + t0;
+        const T* dy = static_cast<const T*>(a.dy) + dense;
+        u32x4 hx[HOLD], hd[HOLD];
+        const auto load_x = [&](int i) {
+            const int c = i * R + cr;
+            return c < a.C && n > 0 ? load_piece<T, TAIL>(x + (int64_t)c * a.x_sc, n) : u32x4{0, 0, 0, 0};
+        };
+        const auto load_d = [&](int i) {
+            const int c = i * R + cr;
+            return c < a.C && n > 0 ? load_piece<T, TAIL>(dy + (int64_t)c * a.S, n) : u32x4{0, 0, 0, 0};
+        };
+        const auto piece_x = [&](int i) {
+            if constexpr (NCH > 0) {
+                unpack_again(hx[i]);
+                return hx[i];
+            } else {
+                return load_x(i);
+            }
+        };
+        const auto piece_d = [&](int i) {
+            if constexpr (NCH > 0) {
+                unpack_again(hd[i]);
+                return hd[i];
+            } else {
+                return load_d(i);
+            }
+        };
+        if constexpr (NCH > 0) {
+#pragma unroll
+            for (int i = 0; i < HOLD; ++i) {
+                hx[i] = load_x(i);
+                hd[i] = load_d(i);
+            }
+        }
+        float mean[V], rstd[V], f[2][V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            // tokens past S: xhat = 0 and dy = 0, so they add nothing
+            mean[e] = e < n ? a.mean[(int64_t)bi * a.S + t0 + e] : 0.0f;
+            rstd[e] = e < n ? a.rstd[(int64_t)bi * a.S + t0 + e] : 0.0f;
+            f[0][e] = f[1][e] = 0.0f;
+        }
+#pragma unroll NCH > 0 ? NCH : 1
+        for (int i = 0; i < nch; ++i) {
+            const int c = i * R + cr;
+            float sg = 0.0f, sb = 0.0f;
+            if (c < a.C) {
+                const u32x4 px = piece_x(i);
+                const u32x4 pd = piece_d(i);
+                const float g = (float)static_cast<const T*>(a.gamma)[c];
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float d = Piece<T>::get(pd, e), xh = (Piece<T>::get(px, e) - mean[e]) * rstd[e];
+                    const float gd = d * g;
+                    f[0][e] += gd;
+                    f[1][e] = fmaf(gd, xh, f[1][e]);
+                    sg = fmaf(d, xh, sg);
+                    sb += d;
+                }
+            }
+            if constexpr (NCH > 0) {
+                dg[i] += sg;
+                db[i] += sb;
+            } else {
+                // this thread alone writes the channel's sums of this workgroup
+                sg = token_sum<TL>(sg);
+                sb = token_sum<TL>(sb);
+                if (tl == 0 && c < a.C) {
+                    out[c] = first ? sg : out[c] + sg;
+                    out[a.C + c] = first ? sb : out[a.C + c] + sb;
+                }
+            }
+        }
+        first = false;
+        strip_total<TL, V, 2, NT>(f, red, tot[0]);
+        T* dx = static_cast<T*>(a.y) + dense;
+        float c1[V], c2[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            c1[e] = tot[0][tl * V + e] * a.inv_c;
+            c2[e] = tot[1][tl * V + e] * a.inv_c;
+        }
+#pragma unroll NCH > 0 ? NCH : 1
+        for (int i = 0; i < nch; ++i) {
+            const int c = i * R + cr;
+            if (c < a.C && n > 0) {
+                const u32x4 px = piece_x(i);
+                const u32x4 pd = piece_d(i);
+                const float g = (float)static_cast<const T*>(a.gamma)[c];
+                float o[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float xh = (Piece<T>::get(px, e) - mean[e]) * rstd[e];
+                    o[e] = rstd[e] * (fmaf(Piece<T>::get(pd, e), g, -c1[e]) - xh * c2[e]);
+                }
+                store_piece<T, TAIL>(dx + (int64_t)c * a.S, o, n);
+            }
+        }
+        // the next strip's totals are written only after its own first barrier, which every
+        // thread reaches after the reads above
+    }
+    if constexpr (NCH > 0) {
+#pragma unroll
+        for (int i = 0; i < HOLD; ++i) {
+            const int c = i * R + cr;
+            const float sg = token_sum<TL>(dg[i]), sb = token_sum<TL>(db[i]);
+            if (tl == 0 && c < a.C) {
+                out[c] = sg;
+                out[a.C + c] = sb;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ dgamma and dbeta
+// Adds the workgroups' sums: 32 columns of [2, C] a workgroup, 32 threads a column.
+template <typename T>
+__global__ __launch_bounds__(1024) void layer_norm_columns_kernel(const float* partial, T* dgamma, T* dbeta, int C,
+                                                                  int parts) {
+    __shared__ double red[32][33];
+    const int col = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
+    double s = 0.0;
+    if (col < 2 * C)
+        for (int p = r; p < parts; p += 32) s += (double)partial[(int64_t)p * 2 * C + col];
+    red[r][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (r == 0 && col < 2 * C) {
+#pragma unroll
+        for (int k = 1; k < 32; ++k) s += red[k][threadIdx.x];
+        if (col < C)
+            dgamma[col] = (T)(float)s;
+        else if (dbeta)
+            dbeta[col - C] = (T)(float)s;
+    }
+}
+
+// ------------------------------------------------------------------ plans
+constexpr int64_t kMaxIndex = (int64_t(1) << 31) - 1;
+
+struct Derived {
+    int64_t S = 0, M = 0, C = 0, sb = 0, ss = 0, sc = 0, x_span = 0;
+    bool first = false;
+    int esize = 0, V = 0;
+    int tpr = 0, tl = 0, nt = 0, nch = 0;        // forward
+    int g_tpr = 0, g_tl = 0, g_nt = 0, g_nch = 0, parts = 0;   // backward
+};
+
+int64_t mul_cap(int64_t a, int64_t b) {
+    const int64_t lim = int64_t(1) << 60;
+    if (a < 0 || b < 0) return -1;
+    if (a == 0 || b == 0) return 0;
+    return a > lim / b ? -1 : a * b;
+}
+
+int at_least(int n, std::initializer_list<int> among) {
+    for (int k : among)
+        if (k >= n) return k;
+    return 0;
+}
+
+int check(const layer_norm_desc* d, Derived* out) {
+    if (!d) return FUSED_PROJ_EINVAL;
+    if (d->dtype != FUSED_PROJ_BF16 && d->dtype != FUSED_PROJ_F32) return FUSED_PROJ_EINVAL;
+    if (d->x_layout != FUSED_PROJ_X_CHANNELS_FIRST && d->x_layout != FUSED_PROJ_X_TOKENS_LAST) return FUSED_PROJ_EINVAL;
+    if (d->batch < 0 || d->channels < 1) return FUSED_PROJ_EINVAL;
+    if (d->x_layout == FUSED_PROJ_X_TOKENS_LAST ? d->n_spatial != 1 : (d->n_spatial < 1 || d->n_spatial > 3))
+        return FUSED_PROJ_EINVAL;
+    if (d->x_stride_batch < 0 || d->x_stride_channel < 0) return FUSED_PROJ_EINVAL;
+    for (int i = 0; i < d->n_spatial; ++i)
+        if (d->spatial[i] < 0 || d->x_stride_spatial[i] < 0) return FUSED_PROJ_EINVAL;
+    if (d->has_bias != 0 && d->has_bias != 1) return FUSED_PROJ_EINVAL;
+    if (!(d->eps >= 0.0) || !std::isfinite((float)d->eps)) return FUSED_PROJ_EINVAL;
+    Derived r;
+    r.esize = d->dtype == FUSED_PROJ_BF16 ? 2 : 4;
+    r.V = 16 / r.esize;
+    r.C = d->channels;
+    r.first = d->x_layout == FUSED_PROJ_X_CHANNELS_FIRST;
+    r.S = 1;
+    for (int i = 0; i < d->n_spatial; ++i) {
+        r.S = mul_cap(r.S, d->spatial[i]);
+        if (r.S < 0) return FUSED_PROJ_EUNSUPPORTED;
+    }
+    r.M = mul_cap(d->batch, r.S);
+    if (r.M < 0 || r.M > kMaxIndex || r.S > kMaxIndex || r.C > kMaxIndex || mul_cap(r.M, r.C) < 0)
+        return FUSED_PROJ_EUNSUPPORTED;
+    r.sb = d->x_stride_batch;
+    r.sc = d->x_stride_channel;
+    if (!r.first) {
+        r.ss = d->x_stride_spatial[0];
+        if (r.M > 0 && r.C > 1 && r.sc != 1) return FUSED_PROJ_EUNSUPPORTED;
+        r.sc = 1;
+        if (r.C > 32768) return FUSED_PROJ_EUNSUPPORTED;
+    } else {
+        int64_t expect = 1;
+        for (int i = d->n_spatial - 1; i >= 0; --i) {
+            if (r.M > 0 && d->spatial[i] > 1 && d->x_stride_spatial[i] != expect) return FUSED_PROJ_EUNSUPPORTED;
+            expect *= d->spatial[i];
+        }
+        r.ss = 1;
+    }
+    if (r.M > 0) {
+        const int64_t a = mul_cap(d->batch - 1, r.sb), b = mul_cap(r.S - 1, r.ss), c = mul_cap(r.C - 1, r.sc);
+        if (a < 0 || b < 0 || c < 0) return FUSED_PROJ_EUNSUPPORTED;
+        r.x_span = a + b + c + 1;
+    }
+    const int V = r.V, C = (int)r.C;
+    if (!r.first) {
+        // A wave a row while the row fits 4 pieces a lane (no barriers); else a workgroup.
+        const auto pick = [&](int& tpr, int& nch) {
+            tpr = C <= 64 * V * 4 ? 64 : C <= 256 * V * 4 ? 256 : 1024;
+            const int need = (C + tpr * V - 1) / (tpr * V);
+            nch = tpr == 1024 ? at_least(need, {2, 4, 8}) : at_least(need, {1, 2, 3, 4});
+        };
+        pick(r.tpr, r.nch);
+        pick(r.g_tpr, r.g_nch);
+        const int rpb = r.g_tpr < 512 ? 512 / r.g_tpr : 1;
+        const int64_t want = (r.M + rpb - 1) / rpb;
+        r.parts = (int)(want < 512 ? want : 512);
+    } else {
+        r.tl = 8;
+        r.nt = 512;
+        r.nch = at_least((C + 63) / 64, {2, 4, 6, 8, 12, 16});
+        r.g_tl = 4;
+        r.g_nt = 1024;
+        r.g_nch = at_least((C + 255) / 256, {1, 2, 3, 4, 6});
+        const int64_t strips = mul_cap(d->batch, (r.S + r.g_tl * V - 1) / (r.g_tl * V));
+        r.parts = (int)(strips < 256 ? strips : 256);
+    }
+    if (out) *out = r;
+    return FUSED_PROJ_OK;
+}
+
+struct Range {
+    uintptr_t lo, hi;
+};
+Range range(const void* p, int64_t bytes) { return {(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes}; }
+bool overlap(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi; }
+bool misaligned(const void* p, int to) { return reinterpret_cast<uintptr_t>(p) & (uintptr_t)(to - 1); }
+
+}  // namespace
+
+struct layer_norm_plan {
+    layer_norm_desc d;
+    Derived r;
+    int device = -1;
+};
+
+namespace {
+
+int hip_status(hipError_t e) {
+    if (e == hipSuccess) return FUSED_PROJ_OK;
+    fp::set_last_hip_error(e);
+    return FUSED_PROJ_EHIP;
+}
+
+int on_device(const layer_norm_plan* h) {
+    int dev = -1;
+    const int rc = hip_status(hipGetDevice(&dev));
+    if (rc) return rc;
+    return dev == h->device ? FUSED_PROJ_OK : FUSED_PROJ_EINVAL;
+}
+
+NormArgs base_args(const layer_norm_plan* h, const void* x, const void* gamma, int tl) {
+    const Derived& r = h->r;
+    NormArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = x;
+    a.gamma = gamma;
+    a.x_sb = r.sb;
+    a.x_ss = r.ss;
+    a.x_sc = r.sc;
+    a.M = (int32_t)r.M;
+    a.S = (int32_t)r.S;
+    a.C = (int32_t)r.C;
+    a.inv_c = (float)(1.0 / (double)r.C);
+    a.eps = (float)h->d.eps;
+    if (r.first) {
+        a.strips = (int32_t)((r.S + tl * r.V - 1) / (tl * r.V));
+        a.all_strips = (int32_t)(h->d.batch * a.strips);
+        a.div_s = fp::make_fastdiv_u31((uint32_t)a.strips);
+    } else {
+        a.div_s = fp::make_fastdiv_u31((uint32_t)r.S);
+    }
+    return a;
+}
+
+void launch(void (*kernel)(NormArgs), unsigned grid, int block, const NormArgs& a, hipStream_t st) {
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), 0, st, a);
+}
+
+template <typename T, bool TAIL>
+void launch_forward(const Derived& r, const NormArgs& a, hipStream_t st) {
+    if (!r.first) {
+        const int block = r.tpr < 256 ? 256 : r.tpr, rpb = block / r.tpr;
+        const unsigned grid = (unsigned)((r.M + rpb - 1) / rpb);
+#define LN_CASE(N, TPR) \
+    if (r.tpr == TPR && r.nch == N) return launch(layer_norm_rows_kernel<T, N, TPR, TAIL>, grid, block, a, st);
+        LN_CASE(1, 64) LN_CASE(2, 64) LN_CASE(3, 64) LN_CASE(4, 64)
+        LN_CASE(2, 256) LN_CASE(3, 256) LN_CASE(4, 256)
+        LN_CASE(2, 1024) LN_CASE(4, 1024)
+        if constexpr (sizeof(T) == 4) LN_CASE(8, 1024)
+#undef LN_CASE
+    } else {
+        const unsigned grid = (unsigned)a.all_strips;
+#define LN_CASE(N) if (r.nch == N) return launch(layer_norm_strips_kernel<T, N, 8, 512, TAIL>, grid, 512, a, st);
+        LN_CASE(2) LN_CASE(4) LN_CASE(6) LN_CASE(8) LN_CASE(12) LN_CASE(16) LN_CASE(0)
+#undef LN_CASE
+    }
+}
+
+template <typename T, bool TAIL>
+void launch_backward(const Derived& r, const NormArgs& a, hipStream_t st) {
+    const unsigned grid = (unsigned)r.parts;
+    if (!r.first) {
+        const int block = r.g_tpr < 512 ? 512 : r.g_tpr;
+#define LN_CASE(N, TPR) \
+    if (r.g_tpr == TPR && r.g_nch == N) \
+        return launch(layer_norm_rows_grad_kernel<T, N, TPR, TAIL>, grid, block, a, st);
+        LN_CASE(1, 64) LN_CASE(2, 64) LN_CASE(3, 64) LN_CASE(4, 64)
+        LN_CASE(2, 256) LN_CASE(3, 256) LN_CASE(4, 256)
+        LN_CASE(2, 1024) LN_CASE(4, 1024)
+        if constexpr (sizeof(T) == 4) LN_CASE(8, 1024)
+#undef LN_CASE
+    } else {
+#define LN_CASE(N) \
+    if (r.g_nch == N) return launch(layer_norm_strips_grad_kernel<T, N, 4, 1024, TAIL>, grid, 1024, a, st);
+        LN_CASE(1) LN_CASE(2) LN_CASE(3) LN_CASE(4) LN_CASE(6) LN_CASE(0)
+#undef LN_CASE
+    }
+}
+
+// Whether a vector piece can end past the row (token-major: C) or the slab's tokens
+// (channels-first: S).
+bool has_tail(const Derived& r) { return (r.first ? r.S : r.C) % r.V != 0; }
+
+}  // namespace
+
+extern "C" {
+
+int layer_norm_validate(const layer_norm_desc* desc) { return check(desc, nullptr); }
+
+int layer_norm_create(const layer_norm_desc* desc, layer_norm_t* out) {
+    if (!out) return FUSED_PROJ_EINVAL;
+    *out = nullptr;
+    Derived r;
+    int rc = check(desc, &r);
+    if (rc) return rc;
+    layer_norm_plan* h = new (std::nothrow) layer_norm_plan();
+    if (!h) return FUSED_PROJ_EHIP;
+    h->d = *desc;
+    h->r = r;
+    rc = hip_status(hipGetDevice(&h->device));
+    if (rc) {
+        delete h;
+        return rc;
+    }
+    *out = h;
+    return FUSED_PROJ_OK;
+}
+
+int layer_norm_run(layer_norm_t h, const void* x, const void* gamma, const void* beta, void* y, void* stats,
+                   void* stream) {
+    if (!h) return FUSED_PROJ_EINVAL;
+    const Derived& r = h->r;
+    if (r.M == 0) return FUSED_PROJ_OK;
+    const bool bias = h->d.has_bias;
+    if (!x || !gamma || (bias && !beta) || !y) return FUSED_PROJ_EINVAL;
+    for (const void* p : {x, gamma, bias ? beta : gamma, (const void*)y})
+        if (misaligned(p, r.esize)) return FUSED_PROJ_EALIGN;
+    if (misaligned(stats, 4)) return FUSED_PROJ_EALIGN;
+    const Range ins[3] = {range(x, r.x_span * r.esize), range(gamma, r.C * r.esize),
+                          range(bias ? beta : gamma, r.C * r.esize)};
+    const Range ry = range(y, r.M * r.C * r.esize), rs = range(stats, stats ? r.M * 8 : 0);
+    for (const Range& i : ins)
+        if (overlap(ry, i) || overlap(rs, i)) return FUSED_PROJ_EALIAS;
+    if (overlap(ry, rs)) return FUSED_PROJ_EALIAS;
+    const int rc = on_device(h);
+    if (rc) return rc;
+    NormArgs a = base_args(h, x, gamma, r.tl);
+    a.beta = bias ? beta : nullptr;
+    a.y = y;
+    a.mean = static_cast<float*>(stats);
+    a.rstd = stats ? a.mean + r.M : nullptr;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const bool tail = has_tail(r);
+    if (h->d.dtype == FUSED_PROJ_BF16)
+        tail ? launch_forward<__bf16, true>(r, a, st) : launch_forward<__bf16, false>(r, a, st);
+    else
+        tail ? launch_forward<float, true>(r, a, st) : launch_forward<float, false>(r, a, st);
+    return hip_status(hipGetLastError());
+}
+
+int layer_norm_backward_workspace_size(layer_norm_t h, size_t* bytes) {
+    if (!h || !bytes) return FUSED_PROJ_EINVAL;
+    *bytes = (size_t)h->r.parts * 2 * (size_t)h->r.C * sizeof(float);
+    return FUSED_PROJ_OK;
+}
+
+int layer_norm_backward(layer_norm_t h, const void* x, const void* gamma, const void* stats, const void* dy, void* dx,
+                        void* dgamma, void* dbeta, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!h) return FUSED_PROJ_EINVAL;
+    const Derived& r = h->r;
+    const bool bias = h->d.has_bias;
+    if (!dgamma || (bias && !dbeta)) return FUSED_PROJ_EINVAL;
+    const size_t need = (size_t)r.parts * 2 * (size_t)r.C * sizeof(float);
+    if (r.M > 0) {
+        if (!x || !gamma || !stats || !dy || !dx || !workspace || workspace_bytes < need) return FUSED_PROJ_EINVAL;
+        for (const void* p : {x, gamma, dy, (const void*)dx})
+            if (misaligned(p, r.esize)) return FUSED_PROJ_EALIGN;
+        if (misaligned(stats, 4) || misaligned(workspace, 16)) return FUSED_PROJ_EALIGN;
+    }
+    for (const void* p : {(const void*)dgamma, bias ? (const void*)dbeta : (const void*)dgamma})
+        if (misaligned(p, r.esize)) return FUSED_PROJ_EALIGN;
+    const int64_t cb = r.C * r.esize, nb = r.M * r.C * r.esize;
+    const bool any = r.M > 0;
+    const Range ins[4] = {range(x, any ? r.x_span * r.esize : 0), range(gamma, any ? cb : 0),
+                          range(stats, any ? r.M * 8 : 0), range(dy, nb)};
+    const Range outs[4] = {range(dx, nb), range(dgamma, cb), range(dbeta, bias ? cb : 0),
+                           range(workspace, any ? (int64_t)need : 0)};
+    for (int i = 0; i < 4; ++i) {
+        for (const Range& in : ins)
+            if (overlap(outs[i], in)) return FUSED_PROJ_EALIAS;
+        for (int j = i + 1; j < 4; ++j)
+            if (overlap(outs[i], outs[j])) return FUSED_PROJ_EALIAS;
+    }
+    const int rc = on_device(h);
+    if (rc) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (r.M > 0) {
+        NormArgs a = base_args(h, x, gamma, r.g_tl);
+        a.dy = dy;
+        a.y = dx;
+        a.mean = const_cast<float*>(static_cast<const float*>(stats));
+        a.rstd = a.mean + r.M;
+        a.partial = static_cast<float*>(workspace);
+        const bool tail = has_tail(r);
+        if (h->d.dtype == FUSED_PROJ_BF16)
+            tail ? launch_backward<__bf16, true>(r, a, st) : launch_backward<__bf16, false>(r, a, st);
+        else
+            tail ? launch_backward<float, true>(r, a, st) : launch_backward<float, false>(r, a, st);
+        const int rc2 = hip_status(hipGetLastError());
+        if (rc2) return rc2;
+    }
+    // with no tokens there are no parts, and the sums are 0
+    const dim3 grid((unsigned)((2 * r.C + 31) / 32));
+    if (h->d.dtype == FUSED_PROJ_BF16)
+        hipLaunchKernelGGL((layer_norm_columns_kernel<__bf16>), grid, dim3(1024), 0, st,
+                           static_cast<const float*>(workspace), static_cast<__bf16*>(dgamma),
+                           static_cast<__bf16*>(bias ? dbeta : nullptr), (int)r.C, r.parts);
+    else
+        hipLaunchKernelGGL((layer_norm_columns_kernel<float>), grid, dim3(1024), 0, st,
+                           static_cast<const float*>(workspace), static_cast<float*>(dgamma),
+                           static_cast<float*>(bias ? dbeta : nullptr), (int)r.C, r.parts);
+    return hip_status(hipGetLastError());
+}
+
+int layer_norm_destroy(layer_norm_t h) {
+    delete h;
+    return FUSED_PROJ_OK;
+}
+
+}  // extern "C"
