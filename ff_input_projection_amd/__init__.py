@@ -18,8 +18,9 @@ import os
 
 import torch
 
-__all__ = ["FusedProjection", "FusedProjError", "SplitRope", "LayerNorm", "load_library", "LIB_PATH",
-           "EXPORTED_SYMBOLS", "LAYER_NORM_SYMBOLS", "Desc", "SplitRopeDesc", "LayerNormDesc"]
+__all__ = ["FusedProjection", "FusedProjError", "SplitRope", "LayerNorm", "KVCache", "load_library",
+           "LIB_PATH", "EXPORTED_SYMBOLS", "LAYER_NORM_SYMBOLS", "KV_CACHE_SYMBOLS", "Desc", "SplitRopeDesc",
+           "LayerNormDesc", "KVCacheDesc"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libfused_proj.so")
@@ -33,6 +34,9 @@ EXPORTED_SYMBOLS = ["fused_proj_validate", "fused_proj_create", "fused_proj_run"
 # include/layer_norm.h
 LAYER_NORM_SYMBOLS = ["layer_norm_validate", "layer_norm_create", "layer_norm_run", "layer_norm_backward_workspace_size",
                       "layer_norm_backward", "layer_norm_destroy"]
+# include/kv_cache.h
+KV_CACHE_SYMBOLS = ["kv_cache_validate", "kv_cache_create", "kv_cache_storage_bytes", "kv_cache_write", "kv_cache_read",
+                    "kv_cache_attend_workspace_size", "kv_cache_attend", "kv_cache_destroy"]
 
 OK, EINVAL, EUNSUPPORTED, EALIGN, EALIAS, EHIP, ESCRATCH = 0, -1, -2, -3, -4, -5, -6
 BF16, F32 = 0, 1
@@ -77,6 +81,21 @@ class LayerNormDesc(ctypes.Structure):
         ("x_stride_channel", ctypes.c_int64), ("x_stride_spatial", ctypes.c_int64 * 3), ("has_bias", ctypes.c_int32),
         ("eps", ctypes.c_double),
     ]
+
+
+class KVCacheDesc(ctypes.Structure):
+    """Mirror of ``kv_cache_desc``."""
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("bits", ctypes.c_int32), ("batch", ctypes.c_int64), ("tokens", ctypes.c_int64),
+        ("n_heads", ctypes.c_int64), ("n_kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+        ("page_size", ctypes.c_int64), ("n_pages", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+        ("sm_scale", ctypes.c_double),
+    ]
+
+
+class KVCacheStorage(ctypes.Structure):
+    """Mirror of ``kv_cache_storage``."""
+    _fields_ = [(name, ctypes.c_void_p) for name in ("k_codes", "k_params", "v_codes", "v_params")]
 
 
 class FusedProjError(RuntimeError):
@@ -139,6 +158,17 @@ def load_library():
     lib.layer_norm_backward.restype = ctypes.c_int
     lib.layer_norm_destroy.argtypes = [vp]
     lib.layer_norm_destroy.restype = ctypes.c_int
+    size_p, storage_p = ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(KVCacheStorage)
+    lib.kv_cache_validate.argtypes = [ctypes.POINTER(KVCacheDesc)]
+    lib.kv_cache_create.argtypes = [ctypes.POINTER(KVCacheDesc), ctypes.POINTER(vp)]
+    lib.kv_cache_storage_bytes.argtypes = [vp, size_p, size_p]
+    lib.kv_cache_write.argtypes = [vp, vp, vp, storage_p, vp, vp, vp, vp]
+    lib.kv_cache_read.argtypes = [vp, storage_p, vp, vp, vp, vp, vp, vp]
+    lib.kv_cache_attend_workspace_size.argtypes = [vp, size_p]
+    lib.kv_cache_attend.argtypes = [vp, vp, storage_p, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.kv_cache_destroy.argtypes = [vp]
+    for name in KV_CACHE_SYMBOLS:
+        getattr(lib, name).restype = ctypes.c_int
     lib.fused_proj_mfma_ceiling.argtypes = [ctypes.c_int, ctypes.c_uint, vp, ctypes.c_size_t, vp,
                                             ctypes.POINTER(ctypes.c_double)]
     lib.fused_proj_mfma_ceiling.restype = ctypes.c_int
@@ -496,4 +526,5 @@ class SplitRope:
             pass
 
 
+from .kv_cache import KVCache, make_kv_cache_desc, validate_kv_cache  # noqa: E402
 from .layer_norm import LayerNorm, make_layer_norm_desc, validate_layer_norm  # noqa: E402

@@ -20,7 +20,7 @@ FAST_PARTS = 5
 SOURCES = [os.path.join(CSRC, "fused_proj_api.cpp"), os.path.join(CSRC, "fused_proj_kernels.hip"),
            os.path.join(CSRC, "fused_proj_fast.hip"), os.path.join(CSRC, "split_rope.hip"),
            os.path.join(CSRC, "fused_proj_bwd.hip"), os.path.join(CSRC, "mfma_ceiling.hip"),
-           os.path.join(CSRC, "layer_norm.hip")]
+           os.path.join(CSRC, "layer_norm.hip"), os.path.join(CSRC, "kv_cache.hip"), os.path.join(CSRC, "kv_attend.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
