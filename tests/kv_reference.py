@@ -39,7 +39,7 @@ def positions(length: int, count: int | None, tokens: int, capacity: int):
     return {s: first + s for s in range(count) if 0 <= first + s < capacity}
 
 
-def attend(q, k_rows, v_rows, own, length, group, scale):
+def attend(q, k_rows, v_rows, own, length, group, scale, bits):
     """One sequence. q [H, T, hd] fp64; k_rows, v_rows: (code, scale, zero) [KVH, positions, ...] fp64 with a scale of -1
     where there is no page; own {token: position}; returns (o, tolerance) [T, H, hd]."""
     H, T, hd = q.shape
@@ -63,6 +63,11 @@ def attend(q, k_rows, v_rows, own, length, group, scale):
                 # exp2 in hardware: 2^-22; numerator and denominator each carry the relative error of p
                 rel = 2 * (dx.max() + 2.0 ** -21)
                 terms = (w * vs) @ vc + (w * np.abs(vz)).sum()
-                # probabilities times scale rounded to bf16 (half a step, 2^-8), fp32 sums, one last rounding
-                tol[s, h] = 2.0 ** -8 * np.abs(o[s, h]) + 2.0 ** -8 * ((w * vs) @ vc) + (rel + (len(x) + 40) * U) * terms
+                # The kernel sums b (c - C) + p (z + C s) with b = p s rounded to bf16 and C the middle code: b = p s (1 + d),
+                # |d| <= 2^-8 (half a step), so the sum is off by d p s (c - C) a position. Both sums, and C sum b apart, are
+                # fp32 sums of terms of up to p s (c + C) + p |z|. One last rounding.
+                mid = (2 ** bits - 1) / 2
+                off = (w * vs) @ np.abs(vc - mid)
+                terms = terms + 2 * mid * (w * vs).sum()
+                tol[s, h] = 2.0 ** -8 * np.abs(o[s, h]) + 2.0 ** -8 * off + (rel + (len(x) + 40) * U) * terms
     return o, tol

@@ -66,7 +66,8 @@ class Case:
             own = {s: p for s, p in own.items()}
             k, v = ([c[i].astype(np.float64), s[i].astype(np.float64), z[i].astype(np.float64)] for c, s, z in self.rows)
             k[1] = np.where(gone[i].numpy().repeat(self.page)[None, :], -1.0, k[1])
-            out.append(ref.attend(q64[i], k, v, own, length, self.heads // self.kvh, self.scale))
+            out.append(ref.attend(q64[i], k, v, own, length, self.heads // self.kvh, self.scale,
+                                  self.bits))
         return np.stack([o for o, _ in out]), np.stack([t for _, t in out])
 
     def queries(self):
@@ -489,7 +490,7 @@ def test_a_block_in_serving(bits):
         q64 = q.double().cpu().numpy().reshape(b, heads, tokens, hd)
         for i in range(b):
             own = ref.positions(lengths_now[i], counts[i], tokens, 32)
-            want, tol = ref.attend(q64[i], *([a[i] for a in r] for r in rows), own, lengths_now[i], heads // kvh, hd ** -0.5)
+            want, tol = ref.attend(q64[i], *([a[i] for a in r] for r in rows), own, lengths_now[i], heads // kvh, hd ** -0.5, bits)
             within(o[i].double().cpu().numpy().reshape(tokens, heads, hd), want, tol)
             w = w_out.double().cpu().numpy()
             flat, ftol = want.reshape(tokens, -1), tol.reshape(tokens, -1)
