@@ -20,6 +20,7 @@
 #include <cstdint>
 #include <cstring>
 #include <new>
+#include <type_traits>
 
 #include "../../include/layer_norm.h"
 #include "fused_proj_kernels.h"
@@ -73,6 +74,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void layer_norm_rows_kernel(
     constexpr int V = Piece<T>::V, BLOCK = TPR < 256 ? 256 : TPR, RPB = BLOCK / TPR;
     __shared__ float red[TPR > 64 ? TPR / 64 : 1];
     const int lane = threadIdx.x % TPR;
+    // only the last piece can end past the row (NCH is the least that covers it, but at 1024)
+    const auto whole = [](int i) { return !TAIL || (TPR < 1024 && i < NCH - 1); };
     const T* gamma = static_cast<const T*>(a.gamma);
     const T* beta = static_cast<const T*>(a.beta);
     for (int row = blockIdx.x * RPB + threadIdx.x / TPR; row < a.M; row += gridDim.x * RPB) {
@@ -83,7 +86,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void layer_norm_rows_kernel(
         for (int i = 0; i < NCH; ++i) {
             const int c = (i * TPR + lane) * V;
             h[i] = u32x4{0, 0, 0, 0};
-            if (c < a.C) h[i] = load_piece<T, TAIL>(x + c, a.C - c);
+            if ((TPR < 1024 && i < NCH - 1) || c < a.C) h[i] = load_piece(x + c, a.C - c, whole(i));
         }
 #pragma unroll
         for (int i = 0; i < NCH; ++i)
@@ -99,7 +102,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void layer_norm_rows_kernel(
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     const float d = Piece<T>::get(h[i], e) - mean;
-                    if (!TAIL || e < n) sq = fmaf(d, d, sq);
+                    if (whole(i) || e < n) sq = fmaf(d, d, sq);
                 }
             }
         }
@@ -110,13 +113,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void layer_norm_rows_kernel(
             const int c = (i * TPR + lane) * V, n = a.C - c;
             unpack_again(h[i]);
             if (n > 0) {
-                const u32x4 g = load_piece<T, TAIL>(gamma + c, n);
-                const u32x4 b = beta ? load_piece<T, TAIL>(beta + c, n) : u32x4{0, 0, 0, 0};
+                const u32x4 g = load_piece(gamma + c, n, whole(i));
+                const u32x4 b = beta ? load_piece(beta + c, n, whole(i)) : u32x4{0, 0, 0, 0};
                 float o[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e)
                     o[e] = fmaf((Piece<T>::get(h[i], e) - mean) * rstd, Piece<T>::get(g, e), Piece<T>::get(b, e));
-                store_piece<T, TAIL>(y + c, o, n);
+                store_piece<T>(y + c, o, n, whole(i));
             }
         }
         if (a.mean && lane == 0) {
@@ -132,6 +135,7 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR) void layer_norm_rows_grad_ke
     __shared__ float red[BLOCK / 64 * 2];
     __shared__ float both[RPB > 1 ? 2 * NCH * TPR * V : 1];
     const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+    const auto whole = [](int i) { return !TAIL || (TPR < 1024 && i < NCH - 1); };
     const T* gamma = static_cast<const T*>(a.gamma);
     float dg[NCH][V], db[NCH][V];
 #pragma unroll
@@ -151,8 +155,8 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR) void layer_norm_rows_grad_ke
             const int c = (i * TPR + lane) * V, n = a.C - c;
             hx[i] = hd[i] = u32x4{0, 0, 0, 0};
             if (real && n > 0) {
-                hx[i] = load_piece<T, TAIL>(x + c, n);
-                hd[i] = load_piece<T, TAIL>(dy + c, n);
+                hx[i] = load_piece(x + c, n, whole(i));
+                hd[i] = load_piece(dy + c, n, whole(i));
             }
         }
         float s1 = 0.0f, s2 = 0.0f;
@@ -160,10 +164,10 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR) void layer_norm_rows_grad_ke
         for (int i = 0; i < NCH; ++i) {
             const int c = (i * TPR + lane) * V, n = a.C - c;
             if (real && n > 0) {
-                const u32x4 g = load_piece<T, TAIL>(gamma + c, n);
+                const u32x4 g = load_piece(gamma + c, n, whole(i));
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    if (!TAIL || e < n) {
+                    if (whole(i) || e < n) {
                         const float d = Piece<T>::get(hd[i], e), xh = (Piece<T>::get(hx[i], e) - mean) * rstd;
                         const float gd = d * Piece<T>::get(g, e);
                         s1 += gd;
@@ -200,14 +204,14 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR) void layer_norm_rows_grad_ke
             unpack_again(hx[i]);
             unpack_again(hd[i]);
             if (real && n > 0) {
-                const u32x4 g = load_piece<T, TAIL>(gamma + c, n);
+                const u32x4 g = load_piece(gamma + c, n, whole(i));
                 float o[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     const float xh = (Piece<T>::get(hx[i], e) - mean) * rstd;
                     o[e] = rstd * (fmaf(Piece<T>::get(hd[i], e), Piece<T>::get(g, e), -s1) - xh * s2);
                 }
-                store_piece<T, TAIL>(dx + c, o, n);
+                store_piece<T>(dx + c, o, n, whole(i));
             }
         }
     }
@@ -293,22 +297,59 @@ __device__ __forceinline__ void strip_total(const float (&f)[NS][V], float* red,
     __syncthreads();
 }
 
-// NCH > 0: the strip is held in registers, NCH pieces a thread. NCH = 0 (more channels than
-// that): it is read again for each use, from the caches.
-template <typename T, int NCH, int TL, int NT, bool TAIL>
+// Workgroups are dispatched round-robin over the 8 XCDs, each with its own L2. Strips that
+// share cache lines (neighbours in a slab) go to workgroups of one XCD.
+__device__ __forceinline__ int strip_of(int bid, int grid) {
+    const int xcd = bid & 7, q = grid >> 3, r = grid & 7;
+    return xcd * q + min(xcd, r) + (bid >> 3);
+}
+
+// The strips of a slab cover its tokens from the first on; the last one is moved back to end
+// with the slab, so that every piece is whole. Its first tokens are then the strip before's
+// too: both compute and store the same bits, and dgamma and dbeta count them once. EDGE: the
+// slab is shorter than a strip, and pieces end with it.
+template <int TT, bool EDGE>
+__device__ __forceinline__ void strip_tokens(const NormArgs& a, int strip, int& bi, int& first, int& twice) {
+    bi = (int)fp::fastdiv_u31((uint32_t)strip, a.div_s);
+    first = (strip - bi * a.strips) * TT;
+    twice = 0;
+    if (!EDGE && first + TT > a.S) {
+        twice = first + TT - a.S;
+        first = a.S - TT;
+    }
+}
+
+// The thread's piece of channel i R + cr: bytes from the slab, a base that the whole workgroup
+// shares; 32 bits of them where the strip is held (the plan has checked that the slab fits),
+// so that no 64-bit address a piece takes registers.
+template <int NCH>
+using Offset = std::conditional_t<(NCH > 0), uint32_t, uint64_t>;
+template <typename T, typename O>
+__device__ __forceinline__ T* at_bytes(T* base, O off) {
+    return reinterpret_cast<T*>(reinterpret_cast<char*>(const_cast<std::remove_const_t<T>*>(base)) + off);
+}
+
+// NCH > 0: the strip is held in registers, NCH pieces a thread (all but the last within C).
+// NCH = 0 (more channels than that, or EDGE): it is read again for each use, from the caches.
+template <typename T, int NCH, int TL, int NT, bool EDGE>
 __global__ __launch_bounds__(NT) void layer_norm_strips_kernel(NormArgs a) {
+    static_assert(!EDGE || NCH == 0, "pieces that end with the slab are not held");
     constexpr int V = Piece<T>::V, R = NT / TL, TT = TL * V, HOLD = NCH > 0 ? NCH : 1;
     __shared__ float red[NT / 64 * TT];
     __shared__ float tot[2][TT];
     const int tl = threadIdx.x % TL, cr = threadIdx.x / TL;
-    const int bi = (int)fp::fastdiv_u31(blockIdx.x, a.div_s), t0 = (int)(blockIdx.x - (uint32_t)bi * a.strips) * TT + tl * V;
-    const int n = a.S - t0;
+    int bi, first, twice;
+    strip_tokens<TT, EDGE>(a, strip_of(blockIdx.x, gridDim.x), bi, first, twice);
+    const int n = EDGE ? a.S - first - tl * V : V;
     const int nch = NCH > 0 ? NCH : (a.C + R - 1) / R;
-    const T* x = static_cast<const T*>(a.x) + (int64_t)bi * a.x_sb + t0;
+    const T* x = static_cast<const T*>(a.x) + (int64_t)bi * a.x_sb + first;
+    T* y = static_cast<T*>(a.y) + (int64_t)bi * a.C * a.S + first;
+    const auto off_x = [&](int i) { return ((Offset<NCH>)(i * R + cr) * (Offset<NCH>)a.x_sc + tl * V) * (Offset<NCH>)sizeof(T); };
+    const auto off_y = [&](int i) { return ((Offset<NCH>)(i * R + cr) * (Offset<NCH>)a.S + tl * V) * (Offset<NCH>)sizeof(T); };
+    const auto inside = [&](int i) { return ((NCH > 0 && i < NCH - 1) || i * R + cr < a.C) && (!EDGE || n > 0); };
     u32x4 h[HOLD];
     const auto load = [&](int i) {
-        const int c = i * R + cr;
-        return c < a.C && n > 0 ? load_piece<T, TAIL>(x + (int64_t)c * a.x_sc, n) : u32x4{0, 0, 0, 0};
+        return inside(i) ? load_piece(at_bytes(x, off_x(i)), n, !EDGE) : u32x4{0, 0, 0, 0};
     };
     if constexpr (NCH > 0) {
 #pragma unroll
@@ -340,7 +381,7 @@ __global__ __launch_bounds__(NT) void layer_norm_strips_kernel(NormArgs a) {
     }
 #pragma unroll NCH > 0 ? NCH : 1
     for (int i = 0; i < nch; ++i) {
-        if (i * R + cr < a.C) {
+        if (inside(i)) {
             const u32x4 p = piece(i);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
@@ -352,26 +393,26 @@ __global__ __launch_bounds__(NT) void layer_norm_strips_kernel(NormArgs a) {
     strip_total<TL, V, 1, NT>(f, red, tot[1]);
 #pragma unroll
     for (int e = 0; e < V; ++e) rstd[e] = 1.0f / sqrtf(tot[1][tl * V + e] * a.inv_c + a.eps);
-    T* y = static_cast<T*>(a.y) + (int64_t)bi * a.C * a.S + t0;
 #pragma unroll NCH > 0 ? NCH : 1
     for (int i = 0; i < nch; ++i) {
         const int c = i * R + cr;
-        if (c < a.C && n > 0) {
+        if (inside(i)) {
             const u32x4 p = piece(i);
             const float g = (float)static_cast<const T*>(a.gamma)[c];
             const float b = a.beta ? (float)static_cast<const T*>(a.beta)[c] : 0.0f;
             float o[V];
 #pragma unroll
             for (int e = 0; e < V; ++e) o[e] = fmaf((Piece<T>::get(p, e) - mean[e]) * rstd[e], g, b);
-            store_piece<T, TAIL>(y + (int64_t)c * a.S, o, n);
+            store_piece<T>(at_bytes(y, off_y(i)), o, n, !EDGE);
         }
     }
     if (a.mean && cr == 0) {
+        const int at = bi * a.S + first + tl * V;   // below b S
 #pragma unroll
         for (int e = 0; e < V; ++e)
-            if (e < n) {
-                a.mean[(int64_t)bi * a.S + t0 + e] = mean[e];
-                a.rstd[(int64_t)bi * a.S + t0 + e] = rstd[e];
+            if (!EDGE || e < n) {
+                a.mean[at + e] = mean[e];
+                a.rstd[at + e] = rstd[e];
             }
     }
 }
@@ -385,122 +426,146 @@ __device__ __forceinline__ float token_sum(float v) {
     return v;
 }
 
-template <typename T, int NCH, int TL, int NT, bool TAIL>
+// A workgroup takes strips in turn. While it writes a strip's dx piece by piece, each
+// register that becomes free takes the next strip's piece: the loads of one strip run under
+// the arithmetic of the one before, with no registers of their own. Loads return in order,
+// so nothing else is loaded in between: gamma stays in registers, and a strip's statistics
+// are fetched ahead of its pieces.
+template <typename T, int NCH, int TL, int NT, bool SHIFT, bool EDGE>
 __global__ __launch_bounds__(NT) void layer_norm_strips_grad_kernel(NormArgs a) {
+    static_assert(!EDGE || NCH == 0, "pieces that end with the slab are not held");
     constexpr int V = Piece<T>::V, R = NT / TL, TT = TL * V, HOLD = NCH > 0 ? NCH : 1;
     __shared__ float red[NT / 64 * 2 * TT];
     __shared__ float tot[2][TT];
+    __shared__ float stats[2][TT];
     const int tl = threadIdx.x % TL, cr = threadIdx.x / TL;
     const int nch = NCH > 0 ? NCH : (a.C + R - 1) / R;
     float* out = a.partial + (int64_t)blockIdx.x * 2 * a.C;
-    float dg[HOLD], db[HOLD];
+    float gamma[HOLD], dg[HOLD], db[HOLD];
 #pragma unroll
-    for (int i = 0; i < HOLD; ++i) dg[i] = db[i] = 0.0f;
-    bool first = true;
-    for (int strip = blockIdx.x; strip < a.all_strips; strip += gridDim.x) {
-        const int bi = (int)fp::fastdiv_u31((uint32_t)strip, a.div_s), t0 = (strip - bi * a.strips) * TT + tl * V;
-        const int n = a.S - t0;
-        const T* x = static_cast<const T*>(a.x) + (int64_t)bi * a.x_sb + t0;
-        const int64_t dense = (int64_t)bi * a.C * a.S + t0;
-        const T* dy = static_cast<const T*>(a.dy) + dense;
-        u32x4 hx[HOLD], hd[HOLD];
-        const auto load_x = [&](int i) {
-            const int c = i * R + cr;
-            return c < a.C && n > 0 ? load_piece<T, TAIL>(x + (int64_t)c * a.x_sc, n) : u32x4{0, 0, 0, 0};
-        };
-        const auto load_d = [&](int i) {
-            const int c = i * R + cr;
-            return c < a.C && n > 0 ? load_piece<T, TAIL>(dy + (int64_t)c * a.S, n) : u32x4{0, 0, 0, 0};
-        };
-        const auto piece_x = [&](int i) {
-            if constexpr (NCH > 0) {
-                unpack_again(hx[i]);
-                return hx[i];
-            } else {
-                return load_x(i);
-            }
-        };
-        const auto piece_d = [&](int i) {
-            if constexpr (NCH > 0) {
-                unpack_again(hd[i]);
-                return hd[i];
-            } else {
-                return load_d(i);
-            }
-        };
-        if constexpr (NCH > 0) {
+    for (int i = 0; i < HOLD; ++i) {
+        gamma[i] = NCH > 0 && i * R + cr < a.C ? (float)static_cast<const T*>(a.gamma)[i * R + cr] : 0.0f;
+        dg[i] = db[i] = 0.0f;
+    }
+    using Off = Offset<NCH>;
+    const Off lane_x = ((Off)cr * (Off)a.x_sc + tl * V) * sizeof(T), lane_d = ((Off)cr * (Off)a.S + tl * V) * sizeof(T);
+    const Off step_x = (Off)R * (Off)a.x_sc * sizeof(T), step_d = (Off)R * (Off)a.S * sizeof(T);
+    const auto off_x = [&](int i) { return from_here(lane_x) + (Off)i * step_x; };
+    const auto off_d = [&](int i) { return from_here(lane_d) + (Off)i * step_d; };
+    int bi, first, twice, n = V;
+    const T* x;
+    int64_t dense;
+    float stat = 0.0f;
+    const auto go_to = [&](int strip) {
+        strip_tokens<TT, EDGE>(a, strip, bi, first, twice);
+        if (EDGE) n = a.S - first - tl * V;
+        x = static_cast<const T*>(a.x) + (int64_t)bi * a.x_sb + first;
+        dense = (int64_t)bi * a.C * a.S + first;
+        // tokens past S: mean = rstd = 0 and dy = 0, so they add nothing
+        const int t = threadIdx.x % TT;
+        if (threadIdx.x < 2 * TT && (!EDGE || first + t < a.S))
+            stat = (threadIdx.x < TT ? a.mean : a.rstd)[bi * a.S + first + t];   // below b S
+    };
+    const auto inside = [&](int i) { return ((NCH > 0 && i < NCH - 1) || i * R + cr < a.C) && (!EDGE || n > 0); };
+    const auto load_x = [&](int i) {
+        return inside(i) ? load_piece(at_bytes(x, off_x(i)), n, !EDGE) : u32x4{0, 0, 0, 0};
+    };
+    const auto load_d = [&](int i) {
+        return inside(i) ? load_piece(at_bytes(static_cast<const T*>(a.dy) + dense, off_d(i)), n, !EDGE) : u32x4{0, 0, 0, 0};
+    };
+    u32x4 hx[HOLD], hd[HOLD];
+    const int strip0 = strip_of(blockIdx.x, gridDim.x);
+    go_to(strip0);   // there are no more workgroups than strips
+    if constexpr (NCH > 0) {
 #pragma unroll
-            for (int i = 0; i < HOLD; ++i) {
-                hx[i] = load_x(i);
-                hd[i] = load_d(i);
-            }
+        for (int i = 0; i < HOLD; ++i) {
+            hx[i] = load_x(i);
+            hd[i] = load_d(i);
         }
+    }
+    for (int strip = strip0; strip < a.all_strips; strip += gridDim.x) {
+        if (threadIdx.x < 2 * TT) (&stats[0][0])[threadIdx.x] = stat;
+        __syncthreads();
         float mean[V], rstd[V], f[2][V];
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            // tokens past S: xhat = 0 and dy = 0, so they add nothing
-            mean[e] = e < n ? a.mean[(int64_t)bi * a.S + t0 + e] : 0.0f;
-            rstd[e] = e < n ? a.rstd[(int64_t)bi * a.S + t0 + e] : 0.0f;
+            mean[e] = stats[0][tl * V + e];
+            rstd[e] = stats[1][tl * V + e];
             f[0][e] = f[1][e] = 0.0f;
         }
 #pragma unroll NCH > 0 ? NCH : 1
         for (int i = 0; i < nch; ++i) {
             const int c = i * R + cr;
             float sg = 0.0f, sb = 0.0f;
-            if (c < a.C) {
-                const u32x4 px = piece_x(i);
-                const u32x4 pd = piece_d(i);
-                const float g = (float)static_cast<const T*>(a.gamma)[c];
+            if ((NCH > 0 && i < NCH - 1) || c < a.C) {
+                const u32x4 px = NCH > 0 ? hx[NCH > 0 ? i : 0] : load_x(i), pd = NCH > 0 ? hd[NCH > 0 ? i : 0] : load_d(i);
+                const float g = NCH > 0 ? gamma[NCH > 0 ? i : 0] : (float)static_cast<const T*>(a.gamma)[c];
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    const float d = Piece<T>::get(pd, e), xh = (Piece<T>::get(px, e) - mean[e]) * rstd[e];
-                    const float gd = d * g;
+                    float d = Piece<T>::get(pd, e);
+                    const float xh = (Piece<T>::get(px, e) - mean[e]) * rstd[e], gd = d * g;
                     f[0][e] += gd;
                     f[1][e] = fmaf(gd, xh, f[1][e]);
-                    sg = fmaf(d, xh, sg);
-                    sb += d;
+                    if (!SHIFT || tl * V + e >= twice) {
+                        sg = fmaf(d, xh, sg);
+                        sb += d;
+                    }
                 }
             }
             if constexpr (NCH > 0) {
                 dg[i] += sg;
                 db[i] += sb;
+                settle(dg[i]);
+                settle(db[i]);
+                __builtin_amdgcn_sched_barrier(0);
             } else {
                 // this thread alone writes the channel's sums of this workgroup
                 sg = token_sum<TL>(sg);
                 sb = token_sum<TL>(sb);
                 if (tl == 0 && c < a.C) {
-                    out[c] = first ? sg : out[c] + sg;
-                    out[a.C + c] = first ? sb : out[a.C + c] + sb;
+                    out[c] = strip == strip0 ? sg : out[c] + sg;
+                    out[a.C + c] = strip == strip0 ? sb : out[a.C + c] + sb;
                 }
             }
         }
-        first = false;
         strip_total<TL, V, 2, NT>(f, red, tot[0]);
-        T* dx = static_cast<T*>(a.y) + dense;
-        float c1[V], c2[V];
+        // dx = rstd (d gamma - c1 - xhat c2) = d gamma rstd + (x - mean) t2 + t1
+        float t1[V], t2[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            c1[e] = tot[0][tl * V + e] * a.inv_c;
-            c2[e] = tot[1][tl * V + e] * a.inv_c;
+            t1[e] = -rstd[e] * (tot[0][tl * V + e] * a.inv_c);
+            t2[e] = -rstd[e] * (rstd[e] * (tot[1][tl * V + e] * a.inv_c));
         }
+        T* dx = static_cast<T*>(a.y) + dense;
+        const bool more = strip + (int)gridDim.x < a.all_strips;
+        if (NCH > 0 && more) go_to(strip + gridDim.x);
 #pragma unroll NCH > 0 ? NCH : 1
         for (int i = 0; i < nch; ++i) {
-            const int c = i * R + cr;
-            if (c < a.C && n > 0) {
-                const u32x4 px = piece_x(i);
-                const u32x4 pd = piece_d(i);
-                const float g = (float)static_cast<const T*>(a.gamma)[c];
+            if constexpr (NCH > 0) {
+                unpack_again(hx[i]);
+                unpack_again(hd[i]);
+            }
+            if (inside(i)) {
+                const u32x4 px = NCH > 0 ? hx[NCH > 0 ? i : 0] : load_x(i), pd = NCH > 0 ? hd[NCH > 0 ? i : 0] : load_d(i);
+                const float g = NCH > 0 ? gamma[NCH > 0 ? i : 0] : (float)static_cast<const T*>(a.gamma)[i * R + cr];
                 float o[V];
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float xh = (Piece<T>::get(px, e) - mean[e]) * rstd[e];
-                    o[e] = rstd[e] * (fmaf(Piece<T>::get(pd, e), g, -c1[e]) - xh * c2[e]);
+                for (int e = 0; e < V; ++e)
+                    o[e] = fmaf(Piece<T>::get(px, e) - mean[e], t2[e], fmaf(Piece<T>::get(pd, e) * g, rstd[e], t1[e]));
+                store_piece<T>(at_bytes(dx, off_d(i)), o, n, !EDGE);
+                if constexpr (NCH > 0) {
+                    if (more) {
+                        hx[i] = load_x(i);
+                        hd[i] = load_d(i);
+                    }
                 }
-                store_piece<T, TAIL>(dx + (int64_t)c * a.S, o, n);
             }
+            // the refill takes the registers just freed: no load moves up to where it would need others
+            __builtin_amdgcn_sched_barrier(0);
         }
-        // the next strip's totals are written only after its own first barrier, which every
-        // thread reaches after the reads above
+        if (NCH == 0 && more) go_to(strip + gridDim.x);
+        // the next strip's statistics and totals are written where every thread has read this
+        // one's: stats before the totals' barriers, totals before the next statistics'
     }
     if constexpr (NCH > 0) {
 #pragma unroll
@@ -523,8 +588,17 @@ __global__ __launch_bounds__(1024) void layer_norm_columns_kernel(const float* p
     __shared__ double red[32][33];
     const int col = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
     double s = 0.0;
-    if (col < 2 * C)
-        for (int p = r; p < parts; p += 32) s += (double)partial[(int64_t)p * 2 * C + col];
+    if (col < 2 * C) {
+        int p = r;
+        for (; p + 7 * 32 < parts; p += 8 * 32) {   // 8 loads in flight
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = partial[(int64_t)(p + k * 32) * 2 * C + col];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += (double)v[k];
+        }
+        for (; p < parts; p += 32) s += (double)partial[(int64_t)p * 2 * C + col];
+    }
     red[r][threadIdx.x & 31] = s;
     __syncthreads();
     if (r == 0 && col < 2 * C) {
@@ -542,7 +616,7 @@ constexpr int64_t kMaxIndex = (int64_t(1) << 31) - 1;
 
 struct Derived {
     int64_t S = 0, M = 0, C = 0, sb = 0, ss = 0, sc = 0, x_span = 0;
-    bool first = false;
+    bool first = false, edge = false;   // channels-first; its slabs shorter than a strip
     int esize = 0, V = 0;
     int tpr = 0, tl = 0, nt = 0, nch = 0;        // forward
     int g_tpr = 0, g_tl = 0, g_nt = 0, g_nch = 0, parts = 0;   // backward
@@ -620,14 +694,18 @@ int check(const layer_norm_desc* d, Derived* out) {
         const int64_t want = (r.M + rpb - 1) / rpb;
         r.parts = (int)(want < 512 ? want : 512);
     } else {
-        r.tl = 8;
-        r.nt = 512;
-        r.nch = at_least((C + 63) / 64, {2, 4, 6, 8, 12, 16});
-        r.g_tl = 4;
-        r.g_nt = 1024;
-        r.g_nch = at_least((C + 255) / 256, {1, 2, 3, 4, 6});
-        const int64_t strips = mul_cap(d->batch, (r.S + r.g_tl * V - 1) / (r.g_tl * V));
-        r.parts = (int)(strips < 256 ? strips : 256);
+        // as many threads as leave each 6 pieces or fewer
+        r.tl = r.g_tl = 4;
+        r.nt = r.g_nt = C <= 64 * 6 ? 256 : C <= 128 * 6 ? 512 : 1024;
+        const int need = (C + r.nt / 4 - 1) / (r.nt / 4);
+        r.nch = r.g_nch = at_least(need, {1, 2, 3, 4, 5, 6});
+        // held strips: slabs of a strip or more, offsets within a slab in 32 bits of bytes
+        r.edge = r.S < r.tl * V;
+        const int64_t reach = mul_cap(r.C, r.sc > r.S ? r.sc : r.S);
+        if (r.edge || reach < 0 || reach * r.esize > 2 * kMaxIndex) r.nch = r.g_nch = 0;
+        if (r.nch == 0) r.nt = r.g_nt = 1024;
+        const int64_t strips = mul_cap(d->batch, (r.S + r.g_tl * V - 1) / (r.g_tl * V)), turn = 256 * (1024 / r.g_nt);
+        r.parts = (int)(strips < turn ? strips : turn);
     }
     if (out) *out = r;
     return FUSED_PROJ_OK;
@@ -692,49 +770,49 @@ void launch(void (*kernel)(NormArgs), unsigned grid, int block, const NormArgs& 
 }
 
 template <typename T, bool TAIL>
-void launch_forward(const Derived& r, const NormArgs& a, hipStream_t st) {
-    if (!r.first) {
-        const int block = r.tpr < 256 ? 256 : r.tpr, rpb = block / r.tpr;
-        const unsigned grid = (unsigned)((r.M + rpb - 1) / rpb);
-#define LN_CASE(N, TPR) \
-    if (r.tpr == TPR && r.nch == N) return launch(layer_norm_rows_kernel<T, N, TPR, TAIL>, grid, block, a, st);
-        LN_CASE(1, 64) LN_CASE(2, 64) LN_CASE(3, 64) LN_CASE(4, 64)
-        LN_CASE(2, 256) LN_CASE(3, 256) LN_CASE(4, 256)
-        LN_CASE(2, 1024) LN_CASE(4, 1024)
-        if constexpr (sizeof(T) == 4) LN_CASE(8, 1024)
+void launch_rows(const Derived& r, const NormArgs& a, bool grad, hipStream_t st) {
+    const int tpr = grad ? r.g_tpr : r.tpr, nch = grad ? r.g_nch : r.nch;
+    const int block = tpr < (grad ? 512 : 256) ? (grad ? 512 : 256) : tpr, rpb = block / tpr;
+    const unsigned grid = grad ? (unsigned)r.parts : (unsigned)((r.M + rpb - 1) / rpb);
+#define LN_CASE(N, TPR)                                                                         \
+    if (tpr == TPR && nch == N)                                                                 \
+        return launch(grad ? layer_norm_rows_grad_kernel<T, N, TPR, TAIL> : layer_norm_rows_kernel<T, N, TPR, TAIL>, \
+                      grid, block, a, st);
+    LN_CASE(1, 64) LN_CASE(2, 64) LN_CASE(3, 64) LN_CASE(4, 64)
+    LN_CASE(2, 256) LN_CASE(3, 256) LN_CASE(4, 256)
+    LN_CASE(2, 1024) LN_CASE(4, 1024)
+    if constexpr (sizeof(T) == 4) LN_CASE(8, 1024)
 #undef LN_CASE
-    } else {
-        const unsigned grid = (unsigned)a.all_strips;
-#define LN_CASE(N) if (r.nch == N) return launch(layer_norm_strips_kernel<T, N, 8, 512, TAIL>, grid, 512, a, st);
-        LN_CASE(2) LN_CASE(4) LN_CASE(6) LN_CASE(8) LN_CASE(12) LN_CASE(16) LN_CASE(0)
-#undef LN_CASE
-    }
 }
 
-template <typename T, bool TAIL>
-void launch_backward(const Derived& r, const NormArgs& a, hipStream_t st) {
-    const unsigned grid = (unsigned)r.parts;
-    if (!r.first) {
-        const int block = r.g_tpr < 512 ? 512 : r.g_tpr;
-#define LN_CASE(N, TPR) \
-    if (r.g_tpr == TPR && r.g_nch == N) \
-        return launch(layer_norm_rows_grad_kernel<T, N, TPR, TAIL>, grid, block, a, st);
-        LN_CASE(1, 64) LN_CASE(2, 64) LN_CASE(3, 64) LN_CASE(4, 64)
-        LN_CASE(2, 256) LN_CASE(3, 256) LN_CASE(4, 256)
-        LN_CASE(2, 1024) LN_CASE(4, 1024)
-        if constexpr (sizeof(T) == 4) LN_CASE(8, 1024)
+template <typename T>
+void launch_strips(const Derived& r, const NormArgs& a, bool grad, hipStream_t st) {
+    const unsigned grid = grad ? (unsigned)r.parts : (unsigned)a.all_strips;
+    const bool shift = r.S % (4 * Piece<T>::V) != 0;
+    if (r.edge)
+        return launch(grad ? layer_norm_strips_grad_kernel<T, 0, 4, 1024, false, true> : layer_norm_strips_kernel<T, 0, 4, 1024, true>,
+                      grid, 1024, a, st);
+#define LN_CASE(N, NT)                                                                                   \
+    if (r.nt == NT && r.nch == N)                                                                        \
+        return launch(!grad   ? layer_norm_strips_kernel<T, N, 4, NT, false>                             \
+                      : shift ? layer_norm_strips_grad_kernel<T, N, 4, NT, true, false>                  \
+                              : layer_norm_strips_grad_kernel<T, N, 4, NT, false, false>,                \
+                      grid, NT, a, st);
+    LN_CASE(1, 256) LN_CASE(2, 256) LN_CASE(3, 256) LN_CASE(4, 256) LN_CASE(5, 256) LN_CASE(6, 256)
+    LN_CASE(4, 512) LN_CASE(5, 512) LN_CASE(6, 512)
+    LN_CASE(4, 1024) LN_CASE(5, 1024) LN_CASE(6, 1024) LN_CASE(0, 1024)
 #undef LN_CASE
-    } else {
-#define LN_CASE(N) \
-    if (r.g_nch == N) return launch(layer_norm_strips_grad_kernel<T, N, 4, 1024, TAIL>, grid, 1024, a, st);
-        LN_CASE(1) LN_CASE(2) LN_CASE(3) LN_CASE(4) LN_CASE(6) LN_CASE(0)
-#undef LN_CASE
-    }
 }
 
-// Whether a vector piece can end past the row (token-major: C) or the slab's tokens
-// (channels-first: S).
-bool has_tail(const Derived& r) { return (r.first ? r.S : r.C) % r.V != 0; }
+template <typename T>
+void launch_any(const Derived& r, const NormArgs& a, bool grad, hipStream_t st) {
+    if (r.first)
+        launch_strips<T>(r, a, grad, st);
+    else if (r.C % r.V != 0)   // the last piece ends past the row
+        launch_rows<T, true>(r, a, grad, st);
+    else
+        launch_rows<T, false>(r, a, grad, st);
+}
 
 }  // namespace
 
@@ -785,11 +863,10 @@ int layer_norm_run(layer_norm_t h, const void* x, const void* gamma, const void*
     a.mean = static_cast<float*>(stats);
     a.rstd = stats ? a.mean + r.M : nullptr;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const bool tail = has_tail(r);
     if (h->d.dtype == FUSED_PROJ_BF16)
-        tail ? launch_forward<__bf16, true>(r, a, st) : launch_forward<__bf16, false>(r, a, st);
+        launch_any<__bf16>(r, a, false, st);
     else
-        tail ? launch_forward<float, true>(r, a, st) : launch_forward<float, false>(r, a, st);
+        launch_any<float>(r, a, false, st);
     return hip_status(hipGetLastError());
 }
 
@@ -836,11 +913,10 @@ int layer_norm_backward(layer_norm_t h, const void* x, const void* gamma, const 
         a.mean = const_cast<float*>(static_cast<const float*>(stats));
         a.rstd = a.mean + r.M;
         a.partial = static_cast<float*>(workspace);
-        const bool tail = has_tail(r);
         if (h->d.dtype == FUSED_PROJ_BF16)
-            tail ? launch_backward<__bf16, true>(r, a, st) : launch_backward<__bf16, false>(r, a, st);
+            launch_any<__bf16>(r, a, true, st);
         else
-            tail ? launch_backward<float, true>(r, a, st) : launch_backward<float, false>(r, a, st);
+            launch_any<float>(r, a, true, st);
         const int rc2 = hip_status(hipGetLastError());
         if (rc2) return rc2;
     }

@@ -36,12 +36,12 @@ struct Piece<float> {
     }
 };
 
-// n (0..V, or more) values at p, the rest 0; a whole piece is one load.
-template <typename T, bool TAIL>
-__device__ __forceinline__ u32x4 load_piece(const T* p, int n) {
+// The first n of V values at p, the rest 0; with `whole`, all V in one load.
+template <typename T>
+__device__ __forceinline__ u32x4 load_piece(const T* p, int n, bool whole) {
     constexpr int V = Piece<T>::V;
     u32x4 r = {0, 0, 0, 0};
-    if (!TAIL || n >= V) {
+    if (whole || n >= V) {
         __builtin_memcpy(&r, p, 16);
     } else {
         float f[V];
@@ -51,11 +51,12 @@ __device__ __forceinline__ u32x4 load_piece(const T* p, int n) {
     }
     return r;
 }
-// The first n of V values to p; the values behind them stay as they were.
-template <typename T, bool TAIL>
-__device__ __forceinline__ void store_piece(T* p, const float (&f)[Piece<T>::V], int n) {
+// The first n of V values to p (all of them with `whole`); the values behind them stay as
+// they were.
+template <typename T>
+__device__ __forceinline__ void store_piece(T* p, const float (&f)[Piece<T>::V], int n, bool whole) {
     constexpr int V = Piece<T>::V;
-    if (!TAIL || n >= V) {
+    if (whole || n >= V) {
         const u32x4 r = Piece<T>::pack(f);
         __builtin_memcpy(p, &r, 16);
     } else {
@@ -67,7 +68,18 @@ __device__ __forceinline__ void store_piece(T* p, const float (&f)[Piece<T>::V],
 
 // Makes a held piece opaque: the compiler unpacks it again for the next use instead of
 // keeping its V unpacked values in registers since the last one.
-__device__ __forceinline__ void unpack_again(u32x4& r) { asm("" : "+v"(r)); }
+__device__ __forceinline__ void unpack_again(u32x4& r) { asm volatile("" : "+v"(r)); }
+
+// Makes the compiler compute x here: a sum that is needed only behind a loop would else be
+// added up at the loop's end, its terms kept in registers until there.
+__device__ __forceinline__ void settle(float& x) { asm volatile("" : "+v"(x)); }
+// The same value, computed from here on: what depends on it is not moved out of a loop (an
+// offset widened to 64 bits there would take two registers, and the short form of a load).
+__device__ __forceinline__ uint32_t from_here(uint32_t x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+__device__ __forceinline__ uint64_t from_here(uint64_t x) { return x; }
 
 template <int CTRL>
 __device__ __forceinline__ float dpp(float x) {
