@@ -176,6 +176,29 @@ def load_library():
     return lib
 
 
+_calls = None
+
+
+def _planned_calls():
+    """The module ``_call`` (torch_call.cpp): C functions of the library on tensors, in one step."""
+    global _calls
+    if _calls is None:
+        from . import _call
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _call.set_raw_stream(raw if raw is not None else lambda i: torch.cuda.current_stream(i).cuda_stream)
+        _calls = _call
+    return _calls
+
+
+def _planned_call(function: str, handle, slots):
+    return _planned_calls().plan(ctypes.cast(getattr(load_library(), function), ctypes.c_void_p).value, handle.value,
+                                 slots)
+
+
+def _planned_call_function():
+    return _planned_calls().call
+
+
 def _check_single_hip_runtime():
     # torch ships its own libamdhip64 (same SONAME). torch is imported before the
     # library is opened, so the loader binds the library to torch's runtime: one

@@ -15,6 +15,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libfused_proj.so")
+CALL = os.path.join(PKG, "_call.so")
 OBJDIR = os.path.join(PKG, "_build")
 FAST_PARTS = 5
 SOURCES = [os.path.join(CSRC, "fused_proj_api.cpp"), os.path.join(CSRC, "fused_proj_kernels.hip"),
@@ -74,7 +75,29 @@ def build(verbose: bool = False) -> str:
     if rc != 0:
         raise RuntimeError("link failed:\n" + "\n".join(msgs))
     os.replace(tmp, LIB)
+    build_call(verbose)
     return LIB
+
+
+def build_call(verbose: bool = False) -> str:
+    """Builds the `_call` module (planned C-ABI calls on torch tensors): host code on torch's C++ API."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "torch_call.cpp"),
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", CALL + ".tmp"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    rc, msgs = _run(cmd)
+    if rc != 0:
+        raise RuntimeError("g++ failed:\n" + "\n".join(msgs))
+    os.replace(CALL + ".tmp", CALL)
+    return CALL
 
 
 if __name__ == "__main__":

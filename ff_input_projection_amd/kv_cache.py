@@ -5,7 +5,7 @@ import ctypes
 
 import torch
 
-from . import OK, FusedProjError, KVCacheDesc, KVCacheStorage, _DTYPES, load_library
+from . import OK, FusedProjError, KVCacheDesc, KVCacheStorage, _DTYPES, _planned_call, _planned_call_function, load_library
 from .layer_norm import _allocate_on
 
 
@@ -58,6 +58,20 @@ class KVCache:
         n = ctypes.c_size_t()
         rc = self._lib.kv_cache_attend_workspace_size(self._h, ctypes.byref(n))
         self._workspace_bytes = int(n.value) if rc == OK else None   # None: a head size attention does not take
+        # the usual calls (outputs allocated, the current stream) in one step; whatever they do not
+        # take goes through the checks below
+        bf16, i32 = torch.bfloat16, torch.int32
+        store = ("storage", tuple((s, torch.uint8 if i % 2 == 0 else bf16) for i, s in enumerate(self.storage_shapes())))
+        meta = (("in", self._table_shape, None, i32), ("in", (batch,), None, i32), ("maybe", (batch,), None, i32))
+        kv, kv_out = ("in", self._kv_shape, None, bf16), ("out", self._kv_shape, bf16)
+        self._write = _planned_call("kv_cache_write", h, (kv, kv, store, *meta))
+        self._read = _planned_call("kv_cache_read", h, (store, *meta, kv_out, kv_out))
+        self._attend = None
+        if self._workspace_bytes is not None:
+            self._attend = _planned_call("kv_cache_attend", h, (("in", self._q_shape, None, bf16), store, *meta,
+                                                                ("out", self._o_shape, bf16),
+                                                                ("workspace", self._workspace_bytes)))
+        self._call = _planned_call_function()
 
     def storage_shapes(self):
         """Shapes of (k_codes, k_params, v_codes, v_params): codes uint8, params bfloat16 (scale, zero)."""
@@ -98,6 +112,12 @@ class KVCache:
 
     def write(self, storage, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor,
               counts: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> None:
+        if stream is None and self._write is not None:
+            r = self._call(self._write, k, v, storage, table, lengths, counts, None)
+            if type(r) is tuple:
+                return
+            if r is not None:
+                raise FusedProjError(r, "kv_cache_write")
         dev = k.device
         s = self._cache(storage, table, lengths, counts, dev)
         self._check("k", k, self._kv_shape, torch.bfloat16, dev)
@@ -112,6 +132,12 @@ class KVCache:
              stream: torch.cuda.Stream | None = None):
         """(k, v) [batch*KVH, tokens, hd] of the step's tokens, zeros for padding and absent pages. With
         counts = lengths that is all the cache holds, from position 0."""
+        if out is None and stream is None and self._read is not None:
+            r = self._call(self._read, storage, table, lengths, counts, None)
+            if type(r) is tuple:
+                return r
+            if r is not None:
+                raise FusedProjError(r, "kv_cache_read")
         dev = table.device
         s = self._cache(storage, table, lengths, counts, dev)
         if out is None:
@@ -135,6 +161,12 @@ class KVCache:
                workspace: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
         """Attention of the step's queries; the workspace (uint8 device tensor of at least
         workspace_bytes()) is allocated when not given."""
+        if out is None and stream is None and self._attend is not None:
+            r = self._call(self._attend, q, storage, table, lengths, counts, workspace)
+            if type(r) is tuple:
+                return r[0]
+            if r is not None:
+                raise FusedProjError(r, "kv_cache_attend")
         need = self.workspace_bytes()
         dev = q.device
         s = self._cache(storage, table, lengths, counts, dev)
@@ -159,6 +191,7 @@ class KVCache:
 
     def close(self):
         if getattr(self, "_h", None) is not None and self._h.value:
+            self._write = self._read = self._attend = None
             self._lib.kv_cache_destroy(self._h)
             self._h = ctypes.c_void_p()
 

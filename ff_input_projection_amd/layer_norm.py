@@ -6,7 +6,7 @@ import ctypes
 
 import torch
 
-from . import OK, FusedProjError, LayerNormDesc, _DTYPES, _fill_activation, load_library
+from . import OK, FusedProjError, LayerNormDesc, _DTYPES, _fill_activation, _planned_call, _planned_call_function, load_library
 
 
 def make_layer_norm_desc(x_shape, x_strides, layout: str, dtype: torch.dtype, *, eps: float = 1e-5,
@@ -62,6 +62,19 @@ class LayerNorm:
         if rc != OK:
             raise FusedProjError(rc, "layer_norm_backward_workspace_size")
         self._workspace_bytes = int(n.value)
+        # the usual call (outputs allocated, the current stream) in one step; whatever it does not
+        # take goes through the checks below
+        x, c, stats = ("in", self.x_shape, self.x_strides, dtype), ("in", (self.C,), None, dtype), (2, self.M)
+        beta = c if self.has_bias else ("maybe", (self.C,), None, dtype)
+        self._forward = _planned_call("layer_norm_run", h, (x, c, beta, ("out", self.x_shape, dtype),
+                                                            ("out", stats, torch.float32)))
+        self._backward = None
+        if self.has_bias:
+            self._backward = _planned_call(
+                "layer_norm_backward", h,
+                (x, c, ("in", stats, None, torch.float32), ("in", self.x_shape, None, dtype), ("out", self.x_shape, dtype),
+                 ("out", (self.C,), dtype), ("out", (self.C,), dtype), ("workspace", self._workspace_bytes)))
+        self._call = _planned_call_function()
 
     @classmethod
     def for_tensor(cls, x: torch.Tensor, layout: str, **kw) -> "LayerNorm":
@@ -84,6 +97,12 @@ class LayerNorm:
 
     def __call__(self, x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor | None = None, out=None,
                  stream: torch.cuda.Stream | None = None):
+        if out is None and stream is None and self._forward is not None:
+            r = self._call(self._forward, x, gamma, beta if self.has_bias else None, None)
+            if type(r) is tuple:
+                return r
+            if r is not None:
+                raise FusedProjError(r, "layer_norm_run")
         self._check_x(x)
         dev = x.device
         self._check("gamma", gamma, (self.C,), dev)
@@ -110,6 +129,12 @@ class LayerNorm:
         """Gradients (dx, dgamma, dbeta) for the upstream gradient ``dy`` (dense, shaped like x) and
         the forward pass's ``stats``. The workspace (uint8 device tensor of at least
         workspace_bytes()) is allocated when not given."""
+        if out is None and stream is None and self._backward is not None:
+            r = self._call(self._backward, x, gamma, stats, dy, workspace)
+            if type(r) is tuple:
+                return r
+            if r is not None:
+                raise FusedProjError(r, "layer_norm_backward")
         self._check_x(x)
         dev = x.device
         self._check("gamma", gamma, (self.C,), dev)
@@ -141,6 +166,7 @@ class LayerNorm:
 
     def close(self):
         if getattr(self, "_h", None) is not None and self._h.value:
+            self._forward = self._backward = None
             self._lib.layer_norm_destroy(self._h)
             self._h = ctypes.c_void_p()
 
