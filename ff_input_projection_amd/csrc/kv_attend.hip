@@ -75,35 +75,44 @@ __device__ __forceinline__ void load_bytes(uint32_t* w, const uint8_t* p) {
         __builtin_memcpy(w, __builtin_assume_aligned(p, 4), B);
 }
 
+// The pages of a tile's halves, by scalar loads: a tile's own loads wait for them alone.
+struct Pages {
+    int32_t id[2];
+};
+__device__ __forceinline__ Pages pages_of(const CacheArgs& a, const int32_t* table, int tile, int length) {
+    typedef const __attribute__((address_space(4))) int32_t* scalar;
+    Pages g;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int p = tile * 32 + u * 16;
+        g.id[u] = ((scalar)table)[fp::fastdiv_u31((uint32_t)(p < length ? p : 0), a.div_page)];
+    }
+    return g;
+}
+
 template <int D, int BITS>
-__device__ __forceinline__ void load_tile(Tile<D, BITS>& t, const CacheArgs& a, const int32_t* table, int kvh, int tile,
-                                          int length) {
+__device__ __forceinline__ void load_tile(Tile<D, BITS>& t, const CacheArgs& a, const Pages& g, int kvh, int tile, int length) {
     using Sh = Shape<D, BITS>;
     const int lane = threadIdx.x & 63, m = lane & 15, qd = lane >> 4;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
         const int p = tile * 32 + u * 16;
-        int64_t row = 0;   // any row that exists stands in for one that does not
-        t.known[u] = 0;
-        if (p < length) {
-            const int pg = (int)fp::fastdiv_u31((uint32_t)p, a.div_page);
-            const int page = __builtin_amdgcn_readfirstlane(table[pg]);
-            if (page >= 0 && page < a.n_pages) {
-                row = (int64_t)page * a.page_rows + (int64_t)kvh * a.page_size + (p - pg * a.page_size);
-                t.known[u] = length - p < 16 ? length - p : 16;
-            }
-        }
+        const bool there = p < length && (uint32_t)g.id[u] < (uint32_t)a.n_pages;
+        const int in_page = p - (int)fp::fastdiv_u31((uint32_t)p, a.div_page) * a.page_size;
+        // any row that exists stands in for one that does not
+        const int64_t row = there ? (int64_t)g.id[u] * a.page_rows + ((int64_t)kvh * a.page_size + in_page) : 0;
+        t.known[u] = there ? (length - p < 16 ? length - p : 16) : 0;
         const uint8_t* kc = a.k_codes + row * Sh::ROWB;
         const uint8_t* vc = a.v_codes + row * Sh::ROWB;
-        load_bytes<Sh::KW * 4>(t.k[u], kc + (m * Sh::ROWB + qd * (Sh::ROWB / 4)));
+        load_bytes<Sh::KW * 4>(t.k[u], kc + (uint32_t)(m * Sh::ROWB + qd * (Sh::ROWB / 4)));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            load_bytes<Sh::B0>(t.v0[u][j], vc + ((qd * 4 + j) * Sh::ROWB + m * Sh::B0));
+            load_bytes<Sh::B0>(t.v0[u][j], vc + (uint32_t)((qd * 4 + j) * Sh::ROWB + m * Sh::B0));
             if constexpr (Sh::D1 > 0)
-                load_bytes<Sh::B1>(t.v1[u][j], vc + ((qd * 4 + j) * Sh::ROWB + Sh::D0 * BITS / 8 + m * Sh::B1));
+                load_bytes<Sh::B1>(t.v1[u][j], vc + (uint32_t)((qd * 4 + j) * Sh::ROWB + Sh::D0 * BITS / 8 + m * Sh::B1));
         }
-        t.kp[u] = *reinterpret_cast<const u32x4*>(a.k_params + row + qd * 4);
-        t.vp[u] = *reinterpret_cast<const u32x4*>(a.v_params + row + qd * 4);
+        t.kp[u] = *reinterpret_cast<const u32x4*>(a.k_params + row + (uint32_t)(qd * 4));
+        t.vp[u] = *reinterpret_cast<const u32x4*>(a.v_params + row + (uint32_t)(qd * 4));
     }
 }
 
@@ -139,29 +148,137 @@ __device__ __forceinline__ float sum_over_quads(float v) { return swap_sum32(swa
 // A wave's running state.
 template <int D, int R>
 struct State {
-    f32x4 o[R][D / 16];    // output tiles, in codes: see store order at finish()
+    f32x4 o[R][D / 16];    // output tiles, in codes: see each_run
     f32x4 c[R];               // 2 C sum_j b_j, in codes: the same in all four
     float m[R], l[R], z[R];   // running maximum (log2), and this lane's sums of p and of p (z + C s)
 };
+template <int D, int R>
+__device__ __forceinline__ void clear(State<D, R>& st) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        st.m[r] = kLowest;
+        st.l[r] = st.z[r] = 0.0f;
+        st.c[r] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) st.o[r][i] = f32x4{0, 0, 0, 0};
+    }
+}
+
+// The affine part of a lane's 8 positions (two halves of 4): k's scale times the logits'
+// factor, k's zero, v's scale, v's zero + C times its scale.
+struct Affine {
+    float ks[2][4], kz[2][4], vs[2][4], vz[2][4];
+};
+template <int BITS>
+__device__ __forceinline__ float middle(uint32_t w) {
+    return fmaf(param_scale(w), 0.5f * (float)((1 << BITS) - 1), param_zero(w));
+}
+
+// What hides positions from the wave's rows: the halves' existing positions, the tile's first
+// position and each row's own.
+template <int R>
+struct Sight {
+    int known[2], at;
+    int last[R], first_last;
+};
+
+// Probabilities (bf16, times v's scale) of 32 positions from the products s of codes and
+// queries; moves the running maximum where a logit passes it by more than kSlack.
+template <int D, int R>
+__device__ __forceinline__ void probabilities(State<D, R>& st, bf16x8 (&p)[R], const f32x4 (&s)[R][2], const Affine& af,
+                                              const float (&zq)[R], const Sight<R>& sg) {
+    const int qd = (threadIdx.x & 63) >> 4;
+    // whether any of the wave's rows does not see any of the 32 positions
+    const bool edge = sg.known[0] < 16 || sg.known[1] < 16 || sg.at + 31 > sg.first_last;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        bool seen[2][4];
+        if (edge) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) seen[u][i] = qd * 4 + i < sg.known[u] && sg.at + u * 16 + qd * 4 + i <= sg.last[r];
+        }
+        float y[2][4];
+        float top = -INFINITY;
+        const float base = kLift - st.m[r];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                y[u][i] = fmaf(af.ks[u][i], s[r][u][i], fmaf(af.kz[u][i], zq[r], base));
+                if (edge) y[u][i] = seen[u][i] ? y[u][i] : -INFINITY;
+                top = fmaxf(top, y[u][i]);
+            }
+        if (__any(top > kLift + kSlack)) {
+            // the maximum moves: the logits again, without the old one
+            top = kLowest;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    y[u][i] = fmaf(af.ks[u][i], s[r][u][i], af.kz[u][i] * zq[r]);
+                    if (edge) y[u][i] = seen[u][i] ? y[u][i] : -INFINITY;
+                    top = fmaxf(top, y[u][i]);
+                }
+            const float m = fmaxf(st.m[r], max_over_quads(top));
+            const float down = __builtin_amdgcn_exp2f(st.m[r] - m);
+            st.m[r] = m;
+            st.l[r] *= down;
+            st.z[r] *= down;
+            st.c[r] *= down;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) st.o[r][i] *= down;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[u][i] = (y[u][i] - m) + kLift;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float e = __builtin_amdgcn_exp2f(y[u][i]);
+                st.l[r] += e;
+                float es = e * af.vs[u][i], ez = af.vz[u][i];
+                if (edge) {
+                    // a slot that is not seen may hold anything
+                    es = seen[u][i] ? es : 0.0f;
+                    ez = seen[u][i] ? ez : 0.0f;
+                }
+                st.z[r] = fmaf(e, ez, st.z[r]);
+                p[r][u * 4 + i] = (__bf16)es;
+            }
+    }
+}
+
+template <int D, int BITS, int R>
+__device__ __forceinline__ void count_middle(State<D, R>& st, const bf16x8 (&p)[R]) {
+    constexpr uint32_t kTwiceC = ((1u << BITS) - 1) * 0x00010001u;
+    const bf16x8 twice_c = __builtin_bit_cast(bf16x8, u32x4{kTwiceC, kTwiceC, kTwiceC, kTwiceC});
+#pragma unroll
+    for (int r = 0; r < R; ++r) st.c[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(twice_c, p[r], st.c[r], 0, 0, 0);
+}
+
+// Pairs of positions: byte b of two words, each in the low half of 16 bits.
+__device__ __forceinline__ uint32_t byte_pair(uint32_t first, uint32_t second, int b) {
+    return __builtin_amdgcn_perm(second, first, 0x0C040C00u + 0x00010001u * b);
+}
 
 template <int D, int BITS, int R>
 __device__ __forceinline__ void take_tile(State<D, R>& st, const Tile<D, BITS>& t, const bf16x8 (&q)[R][D / 32],
                                           const float (&zq)[R], const int (&last)[R], int first_last, float c1, int tile) {
     using Sh = Shape<D, BITS>;
-    const int qd = (threadIdx.x & 63) >> 4;
-    // whether any of the wave's rows does not see any of the 32 positions
-    const bool edge = t.known[0] < 16 || t.known[1] < 16 || tile * 32 + 31 > first_last;
-    float ks[2][4], kz[2][4], vs[2][4], vz[2][4];
+    Affine af;
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            ks[u][i] = param_scale(t.kp[u][i]) * c1;
-            kz[u][i] = param_zero(t.kp[u][i]);
-            vs[u][i] = param_scale(t.vp[u][i]);
-            vz[u][i] = fmaf(vs[u][i], 0.5f * (float)((1 << BITS) - 1), param_zero(t.vp[u][i]));
+            af.ks[u][i] = param_scale(t.kp[u][i]) * c1;
+            af.kz[u][i] = param_zero(t.kp[u][i]);
+            af.vs[u][i] = param_scale(t.vp[u][i]);
+            af.vz[u][i] = middle<BITS>(t.vp[u][i]);
         }
-    bf16x8 p[R];
     f32x4 s[R][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -174,85 +291,25 @@ __device__ __forceinline__ void take_tile(State<D, R>& st, const Tile<D, BITS>& 
             for (int r = 0; r < R; ++r) s[r][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[r][j], s[r][u], 0, 0, 0);
         }
     }
+    Sight<R> sg;
+    sg.known[0] = t.known[0];
+    sg.known[1] = t.known[1];
+    sg.at = tile * 32;
+    sg.first_last = first_last;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        bool seen[2][4];
-        if (edge) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int at = qd * 4 + i;
-                    seen[u][i] = at < t.known[u] && tile * 32 + u * 16 + at <= last[r];
-                }
-        }
-        float y[2][4];
-        float top = -INFINITY;
-        const float base = kLift - st.m[r];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                y[u][i] = fmaf(ks[u][i], s[r][u][i], fmaf(kz[u][i], zq[r], base));
-                if (edge) y[u][i] = seen[u][i] ? y[u][i] : -INFINITY;
-                top = fmaxf(top, y[u][i]);
-            }
-        if (__any(top > kLift + kSlack)) {
-            // the maximum moves: the logits again, without the old one
-            top = kLowest;
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    y[u][i] = fmaf(ks[u][i], s[r][u][i], kz[u][i] * zq[r]);
-                    if (edge) y[u][i] = seen[u][i] ? y[u][i] : -INFINITY;
-                    top = fmaxf(top, y[u][i]);
-                }
-            const float m = fmaxf(st.m[r], max_over_quads(top));
-            const float down = __builtin_amdgcn_exp2f(st.m[r] - m);
-            st.m[r] = m;
-            st.l[r] *= down;
-            st.z[r] *= down;
-#pragma unroll
-            for (int i = 0; i < Sh::NT; ++i) st.o[r][i] *= down;
-            st.c[r] *= down;
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[u][i] = (y[u][i] - m) + kLift;
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float e = __builtin_amdgcn_exp2f(y[u][i]);
-                st.l[r] += e;
-                float es = e * vs[u][i], ez = vz[u][i];
-                if (edge) {
-                    // a slot that is not seen may hold anything
-                    es = seen[u][i] ? es : 0.0f;
-                    ez = seen[u][i] ? ez : 0.0f;
-                }
-                st.z[r] = fmaf(e, ez, st.z[r]);
-                p[r][u * 4 + i] = (__bf16)es;
-            }
-    }
-    constexpr uint32_t kTwiceC = ((1u << BITS) - 1) * 0x00010001u;
-    const bf16x8 twice_c = __builtin_bit_cast(bf16x8, u32x4{kTwiceC, kTwiceC, kTwiceC, kTwiceC});
-#pragma unroll
-    for (int r = 0; r < R; ++r) st.c[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(twice_c, p[r], st.c[r], 0, 0, 0);
-    // pairs of positions, byte by byte of the lane's part of their rows
+    for (int r = 0; r < R; ++r) sg.last[r] = last[r];
+    bf16x8 p[R];
+    probabilities<D, R>(st, p, s, af, zq, sg);
+    count_middle<D, BITS, R>(st, p);
     const auto part = [&](auto bytes, auto first, const auto& w) {
         constexpr int B = decltype(bytes)::value, T0 = decltype(first)::value;
 #pragma unroll
         for (int b = 0; b < B; ++b) {
-            constexpr uint32_t kPick = 0x0C040C00u;   // {0, byte of the second, 0, byte of the first}
-            const uint32_t sel = kPick + 0x00010001u * (b & 3);
             u32x4 x;
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) x[u * 2 + h] = __builtin_amdgcn_perm(w[u][2 * h + 1][b >> 2], w[u][2 * h][b >> 2], sel);
+                for (int h = 0; h < 2; ++h) x[u * 2 + h] = byte_pair(w[u][2 * h][b >> 2], w[u][2 * h + 1][b >> 2], b & 3);
             if constexpr (BITS == 8) {
 #pragma unroll
                 for (int r = 0; r < R; ++r)
@@ -302,62 +359,38 @@ __device__ __forceinline__ void store_bf16(__bf16* p, const float* v) {
     *reinterpret_cast<bf16xn*>(p) = o;
 }
 
-// WT waves of the workgroup's four take different positions of the same rows; 4 / WT different
-// rows.
-template <int D, int BITS, int R, int WT>
-__global__ __launch_bounds__(256) void kv_attend_kernel(CacheArgs a) {
-    using Sh = Shape<D, BITS>;
-    constexpr int WR = 4 / WT, ROWS = R * 16, PAD = D + 4;
-    __shared__ float both[WT > 1 ? WT * 16 * PAD : 1];
-    __shared__ float both_ml[WT > 1 ? WT * 16 * 2 : 1];
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63, n = lane & 15, qd = lane >> 4;
-    // k/v heads fastest: the workgroups of one share an XCD's L2 where their number is a
-    // multiple of 8; the last rows, which see the most, first
-    const int heads = a.batch * a.KVH;
-    const int head = (int)(blockIdx.x % (uint32_t)heads), rest = (int)(blockIdx.x / (uint32_t)heads);
-    const int split = (int)fp::fastdiv_u31((uint32_t)rest, a.div_blocks);
-    const int block = a.row_blocks - 1 - (rest - split * a.row_blocks);
-    const int seq = (int)fp::fastdiv_u31((uint32_t)head, a.div_kvh), kvh = head - seq * a.KVH;
-    const fp::Step step = fp::step_of(a, seq);
-    const int rows = a.group * a.T;
-    const int row0 = (block * WR + wave / WT) * ROWS;
-
-    // the wave's rows: token of the step, head, position (-1: sees nothing)
-    int last[R], row_out[R];
+// A wave's query rows: R x 16 of the rows of a k/v head, from row0 on.
+template <int D, int BITS, int R>
+struct Rows {
+    int last[R];              // this lane's row: the last position it sees (-1: none)
+    int out[R];               // its place in o, b T H of them (31 bits)
     bool real[R];
-    const __bf16* qrow[R];
+    int first_last;           // the last position that all rows see (below 0: some see none)
+    int sees;                 // positions that any row sees
+    bf16x8 q[R][D / 32];      // the operand: q times 2^lift
+    float zq[R];              // sum q times the logits' factor
+};
+
+// The rows' places and their own positions, and their queries' bits; returns the largest
+// exponent field among the lane's rows whose values are all below 2^90 (others give NaN).
+template <int D, int BITS, int R>
+__device__ __forceinline__ uint32_t find_rows(Rows<D, BITS, R>& w, u32x4 (&raw)[R][D / 32], bool (&bad)[R], const CacheArgs& a,
+                                              const fp::Step& step, int seq, int kvh, int row0) {
+    const int lane = threadIdx.x & 63, n = lane & 15, qd = lane >> 4, rows = a.group * a.T;
+    uint32_t top = 0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int row = row0 + r * 16 + n;
-        real[r] = row < rows;
-        const int s = real[r] ? (int)fp::fastdiv_u31((uint32_t)row, a.div_group) : 0, h = real[r] ? row - s * a.group : 0;
-        last[r] = real[r] && s < step.count ? step.first + s : -1;
+        w.real[r] = row < rows;
+        const int s = w.real[r] ? (int)fp::fastdiv_u31((uint32_t)row, a.div_group) : 0, h = w.real[r] ? row - s * a.group : 0;
+        w.last[r] = w.real[r] && s < step.count ? step.first + s : -1;
         const int qh = kvh * a.group + h;
-        qrow[r] = static_cast<const __bf16*>(a.q) + ((int64_t)(seq * a.H + qh) * a.T + s) * D;
-        row_out[r] = (seq * a.T + s) * a.H + qh;   // b T H fits 31 bits
-    }
-    // the positions that its first and its last real row see: rows are token by token
-    const int s_first = (int)fp::fastdiv_u31((uint32_t)(row0 < rows ? row0 : 0), a.div_group);
-    const int row_end = min(row0 + ROWS, rows) - 1;
-    const int s_last = min((int)fp::fastdiv_u31((uint32_t)max(row_end, 0), a.div_group), step.count - 1);
-    const bool any = row0 < rows && s_first < step.count;
-    // rows that see nothing (padding) are masked by the edge path
-    const int first_last = any && s_last * a.group + a.group - 1 >= row_end ? step.first + s_first : -1;
-    const int sees = any ? max(min(step.length, step.first + s_last + 1), 0) : 0;
-    const int tiles = (sees + 31) >> 5, per = (tiles + a.splits - 1) / a.splits;
-    const int t_begin = split * per, t_end = min(tiles, t_begin + per);
-
-    // q: exponents first
-    u32x4 raw[R][Sh::KS];
-    uint32_t top = 0;
-    bool bad[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
+        w.out[r] = (seq * a.T + s) * a.H + qh;
+        const __bf16* q = static_cast<const __bf16*>(a.q) + ((int64_t)(seq * a.H + qh) * a.T + s) * D + qd * (D / 4);
         uint32_t mine = 0;
 #pragma unroll
-        for (int j = 0; j < Sh::KS; ++j) {
-            raw[r][j] = last[r] >= 0 ? *reinterpret_cast<const u32x4*>(qrow[r] + qd * (D / 4) + j * 8) : u32x4{0, 0, 0, 0};
+        for (int j = 0; j < D / 32; ++j) {
+            raw[r][j] = w.last[r] >= 0 ? *reinterpret_cast<const u32x4*>(q + j * 8) : u32x4{0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < 4; ++i) mine = max(mine, max((raw[r][j][i] >> 7) & 0xFFu, (raw[r][j][i] >> 23) & 0xFFu));
         }
@@ -368,103 +401,360 @@ __global__ __launch_bounds__(256) void kv_attend_kernel(CacheArgs a) {
     }
 #pragma unroll
     for (int k = 1; k < 16; k <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, k));
-    const int e = (int)max(top, 1u) - 127, lift = 100 - e;
-    const float c1 = ldexpf(a.logit_scale, 133 - lift);
-    bf16x8 q[R][Sh::KS];
-    float zq[R];
+    // rows are token by token: the wave's first and last token of the step
+    const int s_first = (int)fp::fastdiv_u31((uint32_t)(row0 < rows ? row0 : 0), a.div_group);
+    const int row_end = min(row0 + R * 16, rows) - 1;
+    const int s_last = min((int)fp::fastdiv_u31((uint32_t)max(row_end, 0), a.div_group), step.count - 1);
+    const bool any = row0 < rows && s_first < step.count;
+    w.first_last = any && s_last * a.group + a.group - 1 >= row_end ? step.first + s_first : -1;
+    w.sees = any ? max(min(step.length, step.first + s_last + 1), 0) : 0;
+    return top;
+}
+template <int D, int BITS, int R>
+__device__ __forceinline__ void lift_rows(Rows<D, BITS, R>& w, const u32x4 (&raw)[R][D / 32], const bool (&bad)[R], int lift,
+                                          float logit_scale) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         float sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < Sh::KS; ++j) {
+        for (int j = 0; j < D / 32; ++j) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float f = bad[r] ? 0.0f : Piece<__bf16>::get(raw[r][j], operand_element<BITS>(i));
                 sum += f;
-                q[r][j][i] = (__bf16)ldexpf(f, BITS == 4 && (i & 2) ? lift - 4 : lift);   // exact
+                w.q[r][j][i] = (__bf16)ldexpf(f, BITS == 4 && (i & 2) ? lift - 4 : lift);   // exact
             }
         }
         sum = sum_over_quads(sum);
-        zq[r] = bad[r] ? NAN : sum * a.logit_scale;
+        w.zq[r] = bad[r] ? NAN : sum * logit_scale;
     }
+}
+// q's lift that brings the exponent field `top` to 2^100, and the factor that takes the
+// products back.
+__device__ __forceinline__ int lift_of(uint32_t top) { return 100 - ((int)max(top, 1u) - 127); }
+__device__ __forceinline__ float logits_factor(int lift, float logit_scale) { return ldexpf(logit_scale, 133 - lift); }
+
+// Which part of the work a workgroup takes. k/v heads run fastest: the workgroups of one
+// share an XCD's L2 where their number is a multiple of 8; the last rows, which see the
+// most, come first.
+struct Share {
+    int seq, kvh, block, split;
+};
+__device__ __forceinline__ Share share_of(const CacheArgs& a) {
+    const int heads = a.batch * a.KVH;
+    const int head = (int)(blockIdx.x % (uint32_t)heads), rest = (int)(blockIdx.x / (uint32_t)heads);
+    Share s;
+    s.split = (int)fp::fastdiv_u31((uint32_t)rest, a.div_blocks);
+    s.block = a.row_blocks - 1 - (rest - s.split * a.row_blocks);
+    s.seq = (int)fp::fastdiv_u31((uint32_t)head, a.div_kvh);
+    s.kvh = head - s.seq * a.KVH;
+    return s;
+}
+
+// Few rows (single and drafted tokens): the four waves of a workgroup hold the same R x 16
+// rows and take different positions, each by itself; at the end they are put together in
+// LDS. Bound by the cache's bytes: the next tile is loaded while one is taken.
+template <int D, int BITS, int R>
+__global__ __launch_bounds__(256) void kv_attend_kernel(CacheArgs a) {
+    constexpr int WT = 4, PAD = D + 4;
+    __shared__ float both[WT * 16 * PAD];
+    __shared__ float both_ml[WT * 16 * 2];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, n = lane & 15, qd = lane >> 4;
+    const Share sh = share_of(a);
+    const fp::Step step = fp::step_of(a, sh.seq);
+    const int rows = a.group * a.T, row0 = sh.block * R * 16;
+    Rows<D, BITS, R> w;
+    float c1;
+    {
+        u32x4 raw[R][D / 32];
+        bool bad[R];
+        const int lift = lift_of(find_rows<D, BITS, R>(w, raw, bad, a, step, sh.seq, sh.kvh, row0));
+        lift_rows<D, BITS, R>(w, raw, bad, lift, a.logit_scale);
+        c1 = logits_factor(lift, a.logit_scale);
+    }
+    const int tiles = (w.sees + 31) >> 5, per = (tiles + a.splits - 1) / a.splits;
+    const int t_begin = sh.split * per, t_end = min(tiles, t_begin + per);
 
     State<D, R> st;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        st.m[r] = kLowest;
-        st.l[r] = st.z[r] = 0.0f;
-        st.c[r] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < Sh::NT; ++i) st.o[r][i] = f32x4{0, 0, 0, 0};
-    }
-    const int32_t* table = a.table + (int64_t)seq * a.max_pages;
-    for (int tile = t_begin + wave % WT; tile < t_end; tile += WT) {
-        Tile<D, BITS> t;
-        load_tile<D, BITS>(t, a, table, kvh, tile, step.length);
-        take_tile<D, BITS, R>(st, t, q, zq, last, first_last, c1, tile);
+    clear<D, R>(st);
+    const int32_t* table = a.table + (int64_t)sh.seq * a.max_pages;
+    // two tiles in turn: one is loaded while the other is taken, and the pages of the next are
+    // known before that. Tiles past the end load a row that exists and are not taken.
+    int tile = t_begin + wave;
+    if (tile < t_end) {
+        Tile<D, BITS> even, odd;
+        load_tile<D, BITS>(even, a, pages_of(a, table, tile, step.length), sh.kvh, tile, step.length);
+        Pages next = pages_of(a, table, tile + WT, step.length);
+        while (true) {
+            load_tile<D, BITS>(odd, a, next, sh.kvh, tile + WT, step.length);
+            next = pages_of(a, table, tile + 2 * WT, step.length);
+            take_tile<D, BITS, R>(st, even, w.q, w.zq, w.last, w.first_last, c1, tile);
+            tile += WT;
+            if (tile >= t_end) break;
+            load_tile<D, BITS>(even, a, next, sh.kvh, tile + WT, step.length);
+            next = pages_of(a, table, tile + 2 * WT, step.length);
+            take_tile<D, BITS, R>(st, odd, w.q, w.zq, w.last, w.first_last, c1, tile);
+            tile += WT;
+            if (tile >= t_end) break;
+        }
     }
 
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const float l = sum_over_quads(st.l[r]) * 0x1p-80f, z = fmaf(st.c[r][0], -0x1p52f, sum_over_quads(st.z[r]) * 0x1p-80f);
-        if constexpr (WT == 1) {
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            __bf16* o = static_cast<__bf16*>(a.o) + (int64_t)row_out[r] * D;
-            if (real[r])
-                each_run<D, BITS, R>(st, r, z, [&](int d, auto& v) {
-                    constexpr int N = sizeof(v) / 4;
+        const float l = sum_over_quads(st.l[r]) * 0x1p-80f;
+        const float z = fmaf(st.c[r][0], -0x1p52f, sum_over_quads(st.z[r]) * 0x1p-80f);
+        // the workgroup's waves together, 16 rows at a time
+        if (r > 0) __syncthreads();
+        float* mine = both + (wave * 16 + n) * PAD;
+        each_run<D, BITS, R>(st, r, z, [&](int d, auto& v) {
+            constexpr int N = sizeof(v) / 4;
 #pragma unroll
-                    for (int k = 0; k < N; ++k) v[k] *= inv;
-                    store_bf16<N>(o + d, v);
-                });
-        } else {
-            // the workgroup's waves together, 16 rows at a time
-            if (r > 0) __syncthreads();
-            float* mine = both + (wave * 16 + n) * PAD;
+            for (int k = 0; k < N; ++k) mine[d + k] = v[k];
+        });
+        if (qd == 0) {
+            both_ml[(wave * 16 + n) * 2] = st.m[r];
+            both_ml[(wave * 16 + n) * 2 + 1] = l;
+        }
+        __syncthreads();
+        for (int it = threadIdx.x; it < 16 * (D / 8); it += 256) {
+            const int rr = it / (D / 8), d = it % (D / 8) * 8, row = row0 + r * 16 + rr;
+            if (row >= rows) continue;
+            const int s = (int)fp::fastdiv_u31((uint32_t)row, a.div_group), qh = sh.kvh * a.group + row - s * a.group;
+            const int64_t out = (int64_t)(sh.seq * a.T + s) * a.H + qh;
+            float m = kLowest, f[WT], sum = 0.0f, v[8];
+#pragma unroll
+            for (int k = 0; k < WT; ++k) m = fmaxf(m, both_ml[(k * 16 + rr) * 2]);
+#pragma unroll
+            for (int k = 0; k < WT; ++k) {
+                f[k] = __builtin_amdgcn_exp2f(both_ml[(k * 16 + rr) * 2] - m);
+                sum = fmaf(f[k], both_ml[(k * 16 + rr) * 2 + 1], sum);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[e] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < WT; ++k) v[e] = fmaf(f[k], both[(k * 16 + rr) * PAD + d + e], v[e]);
+            }
+            if (a.splits == 1) {
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= inv;
+                store_bf16<8>(static_cast<__bf16*>(a.o) + out * D + d, v);
+            } else {
+                const int64_t at = (int64_t)sh.split * a.batch * a.T * a.H + out;
+                f32x4* po = reinterpret_cast<f32x4*>(a.part_o + at * D + d);
+                po[0] = f32x4{v[0], v[1], v[2], v[3]};
+                po[1] = f32x4{v[4], v[5], v[6], v[7]};
+                if (d == 0) {
+                    a.part_ml[at * 2] = m;
+                    a.part_ml[at * 2 + 1] = sum;
+                }
+            }
+        }
+    }
+}
+
+// Many rows (a prompt's chunk): the NW waves of a workgroup hold different rows and take the
+// same positions, 16 NW at a time. Bound by the softmax's vector work, so the operands are
+// made once for all waves: each makes those of its 16 positions and puts them in LDS (the
+// matrix cores' operand layout, 16 bytes a lane), two sets in turn with one barrier each,
+// and the bytes of the positions after next are already under way.
+template <int D, int BITS, int NW>
+struct Shared {
+    using Sh = Shape<D, BITS>;
+    u32x4 k[NW][Sh::KS][64];        // a half's K operands
+    u32x4 v[NW / 2][Sh::NT][64];    // 32 positions' V operands
+    float affine[4][NW * 16];
+    int known[NW];
+};
+
+template <int D, int BITS>
+struct Raw {
+    using Sh = Shape<D, BITS>;
+    uint32_t k[Sh::KW], v0[4][Sh::W0], v1[4][Sh::W1 > 0 ? Sh::W1 : 1], kp, vp;
+    int known;
+};
+
+template <int D, int BITS>
+__device__ __forceinline__ void load_raw(Raw<D, BITS>& t, const CacheArgs& a, int page, int kvh, int p, int length) {
+    using Sh = Shape<D, BITS>;
+    const int lane = threadIdx.x & 63, m = lane & 15, qd = lane >> 4;
+    const bool there = p < length && (uint32_t)page < (uint32_t)a.n_pages;
+    const int in_page = p - (int)fp::fastdiv_u31((uint32_t)p, a.div_page) * a.page_size;
+    const int64_t row = there ? (int64_t)page * a.page_rows + ((int64_t)kvh * a.page_size + in_page) : 0;
+    t.known = there ? (length - p < 16 ? length - p : 16) : 0;
+    const uint8_t* kc = a.k_codes + row * Sh::ROWB;
+    const uint8_t* vc = a.v_codes + row * Sh::ROWB;
+    load_bytes<Sh::KW * 4>(t.k, kc + (uint32_t)(m * Sh::ROWB + qd * (Sh::ROWB / 4)));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        load_bytes<Sh::B0>(t.v0[j], vc + (uint32_t)((qd * 4 + j) * Sh::ROWB + m * Sh::B0));
+        if constexpr (Sh::D1 > 0)
+            load_bytes<Sh::B1>(t.v1[j], vc + (uint32_t)((qd * 4 + j) * Sh::ROWB + Sh::D0 * BITS / 8 + m * Sh::B1));
+    }
+    t.kp = a.k_params[row + (uint32_t)m];
+    t.vp = a.v_params[row + (uint32_t)m];
+}
+
+template <int D, int BITS, int NW>
+__device__ __forceinline__ void share_raw(Shared<D, BITS, NW>& to, const Raw<D, BITS>& t, int wave, float c1) {
+    using Sh = Shape<D, BITS>;
+    const int lane = threadIdx.x & 63, u = wave & 1;
+#pragma unroll
+    for (int j = 0; j < Sh::KS; ++j) to.k[wave][j][lane] = __builtin_bit_cast(u32x4, codes_operand<BITS>(&t.k[j * BITS / 4]));
+    const auto part = [&](auto bytes, auto first, const auto& w) {
+        constexpr int B = decltype(bytes)::value, T0 = decltype(first)::value;
+        const auto put = [&](int tile, u32x2 x) { reinterpret_cast<u32x2*>(&to.v[wave >> 1][tile][lane])[u] = x; };
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            u32x2 x;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) x[h] = byte_pair(w[2 * h][b >> 2], w[2 * h + 1][b >> 2], b & 3);
+            if constexpr (BITS == 8) {
+                put(T0 + b, x);
+            } else {
+                put(T0 + 2 * b, x & 0x000F000Fu);
+                put(T0 + 2 * b + 1, x & 0x00F000F0u);
+            }
+        }
+    };
+    part(std::integral_constant<int, Sh::B0>{}, std::integral_constant<int, 0>{}, t.v0);
+    if constexpr (Sh::D1 > 0) part(std::integral_constant<int, Sh::B1>{}, std::integral_constant<int, Sh::D0 / 16>{}, t.v1);
+    if (lane < 16) {
+        to.affine[0][wave * 16 + lane] = param_scale(t.kp) * c1;
+        to.affine[1][wave * 16 + lane] = param_zero(t.kp);
+        to.affine[2][wave * 16 + lane] = param_scale(t.vp);
+        to.affine[3][wave * 16 + lane] = middle<BITS>(t.vp);
+    }
+    if (lane == 0) to.known[wave] = t.known;
+}
+
+template <int D, int BITS, int R, int NW>
+__global__ __launch_bounds__(NW * 64) void kv_attend_chunk_kernel(CacheArgs a) {
+    using Sh = Shape<D, BITS>;
+    constexpr int STEP = NW * 16;
+    __shared__ Shared<D, BITS, NW> sets[2];
+    __shared__ uint32_t tops[NW];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, qd = lane >> 4;
+    const Share sh = share_of(a);
+    const fp::Step step = fp::step_of(a, sh.seq);
+    Rows<D, BITS, R> w;
+    float c1;
+    {
+        u32x4 raw[R][D / 32];
+        bool bad[R];
+        const uint32_t mine = find_rows<D, BITS, R>(w, raw, bad, a, step, sh.seq, sh.kvh, (sh.block * NW + wave) * R * 16);
+        if (lane == 0) tops[wave] = mine;
+        __syncthreads();
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) top = max(top, tops[k]);
+        const int lift = lift_of(top);   // one for the workgroup: K's affine part is shared
+        lift_rows<D, BITS, R>(w, raw, bad, lift, a.logit_scale);
+        c1 = logits_factor(lift, a.logit_scale);
+    }
+    // the workgroup's positions: those of its last real row
+    const int rows = a.group * a.T, row_end = min((sh.block + 1) * NW * R * 16, rows) - 1;
+    const int s_last = min((int)fp::fastdiv_u31((uint32_t)row_end, a.div_group), step.count - 1);
+    const int s_first = (int)fp::fastdiv_u31((uint32_t)(sh.block * NW * R * 16), a.div_group);
+    const int sees = s_first < step.count ? max(min(step.length, step.first + s_last + 1), 0) : 0;
+    const int turns = (sees + STEP - 1) / STEP, per = (turns + a.splits - 1) / a.splits;
+    const int t_begin = sh.split * per, t_end = min(turns, t_begin + per);
+
+    State<D, R> st;
+    clear<D, R>(st);
+    if (t_begin < t_end) {
+        typedef const __attribute__((address_space(4))) int32_t* scalar;
+        const scalar table = (scalar)(a.table + (int64_t)sh.seq * a.max_pages);
+        const auto place = [&](int turn) { return turn * STEP + wave * 16; };
+        const auto page_of = [&](int turn) {
+            const int p = place(turn);
+            return table[fp::fastdiv_u31((uint32_t)(p < step.length ? p : 0), a.div_page)];
+        };
+        Raw<D, BITS> raw;
+        load_raw<D, BITS>(raw, a, page_of(t_begin), sh.kvh, place(t_begin), step.length);
+        share_raw<D, BITS, NW>(sets[0], raw, wave, c1);
+        load_raw<D, BITS>(raw, a, page_of(t_begin + 1), sh.kvh, place(t_begin + 1), step.length);
+        int page = page_of(t_begin + 2);
+        __syncthreads();
+        for (int turn = t_begin; turn < t_end; ++turn) {
+            const Shared<D, BITS, NW>& now = sets[(turn - t_begin) & 1];
+            // the other set was read before the last barrier
+            if (turn + 1 < t_end) share_raw<D, BITS, NW>(sets[(turn + 1 - t_begin) & 1], raw, wave, c1);
+            load_raw<D, BITS>(raw, a, page, sh.kvh, place(turn + 2), step.length);
+            page = page_of(turn + 3);
+#pragma unroll 1
+            for (int g = 0; g < NW / 2; ++g) {
+                Sight<R> sg;
+                sg.at = turn * STEP + g * 32;
+                if (sg.at >= w.sees) break;   // this wave's rows see nothing from here on
+                sg.known[0] = __builtin_amdgcn_readfirstlane(now.known[2 * g]);
+                sg.known[1] = __builtin_amdgcn_readfirstlane(now.known[2 * g + 1]);
+                sg.first_last = w.first_last;
+#pragma unroll
+                for (int r = 0; r < R; ++r) sg.last[r] = w.last[r];
+                f32x4 s[R][2];
+                Affine af;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r) s[r][u] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int j = 0; j < Sh::KS; ++j) {
+                        const bf16x8 k = __builtin_bit_cast(bf16x8, now.k[2 * g + u][j][lane]);
+#pragma unroll
+                        for (int r = 0; r < R; ++r) s[r][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, w.q[r][j], s[r][u], 0, 0, 0);
+                    }
+                    const int at = (2 * g + u) * 16 + qd * 4;
+                    const f32x4 ks = *reinterpret_cast<const f32x4*>(&now.affine[0][at]), kz = *reinterpret_cast<const f32x4*>(&now.affine[1][at]);
+                    const f32x4 vs = *reinterpret_cast<const f32x4*>(&now.affine[2][at]), vz = *reinterpret_cast<const f32x4*>(&now.affine[3][at]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        af.ks[u][i] = ks[i];
+                        af.kz[u][i] = kz[i];
+                        af.vs[u][i] = vs[i];
+                        af.vz[u][i] = vz[i];
+                    }
+                }
+                bf16x8 p[R];
+                probabilities<D, R>(st, p, s, af, w.zq, sg);
+                count_middle<D, BITS, R>(st, p);
+#pragma unroll
+                for (int i = 0; i < Sh::NT; ++i) {
+                    const bf16x8 v = __builtin_bit_cast(bf16x8, now.v[g][i][lane]);
+#pragma unroll
+                    for (int r = 0; r < R; ++r) st.o[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[r], st.o[r][i], 0, 0, 0);
+                }
+            }
+            __syncthreads();
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float l = sum_over_quads(st.l[r]) * 0x1p-80f;
+        const float z = fmaf(st.c[r][0], -0x1p52f, sum_over_quads(st.z[r]) * 0x1p-80f);
+        if (!w.real[r]) continue;
+        if (a.splits == 1) {
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            __bf16* o = static_cast<__bf16*>(a.o) + (int64_t)w.out[r] * D;
             each_run<D, BITS, R>(st, r, z, [&](int d, auto& v) {
                 constexpr int N = sizeof(v) / 4;
 #pragma unroll
-                for (int k = 0; k < N; ++k) mine[d + k] = v[k];
+                for (int k = 0; k < N; ++k) v[k] *= inv;
+                store_bf16<N>(o + d, v);
+            });
+        } else {
+            const int64_t at = (int64_t)sh.split * a.batch * a.T * a.H + w.out[r];
+            each_run<D, BITS, R>(st, r, z, [&](int d, auto& v) {
+                constexpr int N = sizeof(v) / 4;
+#pragma unroll
+                for (int k = 0; k < N; ++k) a.part_o[at * D + d + k] = v[k];
             });
             if (qd == 0) {
-                both_ml[(wave * 16 + n) * 2] = st.m[r];
-                both_ml[(wave * 16 + n) * 2 + 1] = l;
-            }
-            __syncthreads();
-            for (int it = threadIdx.x; it < 16 * (D / 8); it += 256) {
-                const int rr = it / (D / 8), d = it % (D / 8) * 8, row = row0 + r * 16 + rr;
-                if (row >= rows) continue;
-                const int s = (int)fp::fastdiv_u31((uint32_t)row, a.div_group), qh = kvh * a.group + row - s * a.group;
-                const int64_t out = (int64_t)(seq * a.T + s) * a.H + qh;
-                float m = kLowest, f[WT], sum = 0.0f, v[8];
-#pragma unroll
-                for (int w = 0; w < WT; ++w) m = fmaxf(m, both_ml[(w * 16 + rr) * 2]);
-#pragma unroll
-                for (int w = 0; w < WT; ++w) {
-                    f[w] = __builtin_amdgcn_exp2f(both_ml[(w * 16 + rr) * 2] - m);
-                    sum = fmaf(f[w], both_ml[(w * 16 + rr) * 2 + 1], sum);
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    v[k] = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < WT; ++w) v[k] = fmaf(f[w], both[(w * 16 + rr) * PAD + d + k], v[k]);
-                }
-                if (a.splits == 1) {
-                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] *= inv;
-                    store_bf16<8>(static_cast<__bf16*>(a.o) + out * D + d, v);
-                } else {
-                    const int64_t at = (int64_t)split * a.batch * a.T * a.H + out;
-                    f32x4* po = reinterpret_cast<f32x4*>(a.part_o + at * D + d);
-                    po[0] = f32x4{v[0], v[1], v[2], v[3]};
-                    po[1] = f32x4{v[4], v[5], v[6], v[7]};
-                    if (d == 0) {
-                        a.part_ml[at * 2] = m;
-                        a.part_ml[at * 2 + 1] = sum;
-                    }
-                }
+                a.part_ml[at * 2] = st.m[r];
+                a.part_ml[at * 2 + 1] = l;
             }
         }
     }
@@ -500,19 +790,21 @@ __global__ __launch_bounds__(256) void kv_attend_join_kernel(CacheArgs a) {
     }
 }
 
+// Rows of a wave of the chunk kernel (in tiles of 16) and the waves of its workgroup, as
+// registers (two waves a SIMD) and LDS (two sets of 16 NW (4 D + 16) bytes) allow.
+template <int D>
+struct Chunk {
+    static constexpr int R = D <= 128 ? 2 : 1, NW = D <= 128 ? 8 : 4;
+};
+
 template <int D, int BITS>
 void launch_shape(const fp::AttendPlan& p, const CacheArgs& a, unsigned grid, hipStream_t st) {
-    constexpr int RL = D <= 128 ? 4 : 2;   // row tiles of a wave that registers hold
-#define KV_CASE(R, WT)                                                                                \
-    if (p.rows_per_wave == R && p.token_waves == WT) {                                                \
-        hipLaunchKernelGGL((kv_attend_kernel<D, BITS, R, WT>), dim3(grid), dim3(256), 0, st, a);      \
-        return;                                                                                       \
-    }
-    KV_CASE(1, 4)
-    KV_CASE(2, 4)
-    if constexpr (RL == 4) KV_CASE(4, 4)
-    KV_CASE(RL, 1)
-#undef KV_CASE
+    if (p.chunk)
+        hipLaunchKernelGGL((kv_attend_chunk_kernel<D, BITS, Chunk<D>::R, Chunk<D>::NW>), dim3(grid), dim3(Chunk<D>::NW * 64), 0, st, a);
+    else if (D > 128 || p.row_tiles == 1)
+        hipLaunchKernelGGL((kv_attend_kernel<D, BITS, 1>), dim3(grid), dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((kv_attend_kernel<D, BITS, D <= 128 ? 2 : 1>), dim3(grid), dim3(256), 0, st, a);
 }
 
 }  // namespace
@@ -522,24 +814,20 @@ namespace fp {
 bool plan_attend(const kv_cache_desc& d, int64_t kvh, AttendPlan* out) {
     const int64_t hd = d.head_dim;
     if (hd != 32 && hd != 64 && hd != 96 && hd != 128 && hd != 192 && hd != 256) return false;
-    const int64_t rows = d.n_heads / kvh * d.tokens, heads = d.batch * kvh;
+    const int64_t rows = d.n_heads / kvh * d.tokens, heads = d.batch * kvh > 0 ? d.batch * kvh : 1;
     AttendPlan p;
-    const int most = hd <= 128 ? 4 : 2;
-    p.rows_per_wave = rows <= 16 ? 1 : rows <= 32 ? 2 : most;
-    const int64_t wide = (rows + p.rows_per_wave * 64 - 1) / (p.rows_per_wave * 64);
-    if (p.rows_per_wave == most && rows > 32 && heads * wide >= 256) {
-        p.token_waves = 1;
-        p.row_blocks = (int32_t)wide;
-        p.splits = 1;
-    } else {
-        p.token_waves = 4;
-        p.row_blocks = (int32_t)((rows + p.rows_per_wave * 16 - 1) / (p.rows_per_wave * 16));
-        const int64_t tiles = (d.max_pages * d.page_size + 31) / 32;
-        int64_t splits = heads > 0 ? (1024 + heads * p.row_blocks - 1) / (heads * p.row_blocks) : 1;
-        if (splits > (tiles + 7) / 8) splits = (tiles + 7) / 8;
-        if (splits > 64) splits = 64;
-        p.splits = (int32_t)(splits < 1 ? 1 : splits);
-    }
+    p.chunk = rows > 32;
+    p.row_tiles = rows <= 16 || hd > 128 ? 1 : 2;   // two tiles of a wider head would spill
+    const int64_t block = p.chunk ? 16 * (hd <= 128 ? Chunk<128>::R * Chunk<128>::NW : Chunk<256>::R * Chunk<256>::NW)
+                                  : 16 * p.row_tiles;
+    p.row_blocks = (int32_t)((rows + block - 1) / block);
+    // Parts of a sequence: enough workgroups to fill the card (4 of 256 threads a CU, one of
+    // the chunk kernel's), each with some tiles a wave.
+    const int64_t positions = d.max_pages * d.page_size, want = p.chunk ? 256 : 1024, least = p.chunk ? 512 : 256;
+    int64_t splits = (want + heads * p.row_blocks - 1) / (heads * p.row_blocks);
+    if (p.chunk && 2 * heads * p.row_blocks > want) splits = 1;
+    if (splits > (positions + least - 1) / least) splits = (positions + least - 1) / least;
+    p.splits = (int32_t)(splits < 1 ? 1 : splits > 64 ? 64 : splits);
     if (p.splits > 1) p.workspace = (size_t)p.splits * (size_t)(d.batch * d.tokens * d.n_heads) * (size_t)(hd + 2) * 4;
     *out = p;
     return true;

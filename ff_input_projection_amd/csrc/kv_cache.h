@@ -50,8 +50,8 @@ __device__ __forceinline__ Step step_of(const CacheArgs& a, int seq) {
 
 // Defined in kv_attend.hip.
 struct AttendPlan {
-    int32_t rows_per_wave = 0;   // in tiles of 16
-    int32_t token_waves = 0;     // waves of a workgroup that take different positions
+    bool chunk = false;          // many rows: kv_attend_chunk_kernel
+    int32_t row_tiles = 0;       // else: rows of a workgroup, in tiles of 16
     int32_t row_blocks = 0, splits = 0;
     size_t workspace = 0;
 };
