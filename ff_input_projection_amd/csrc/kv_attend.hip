@@ -183,45 +183,49 @@ struct Sight {
 };
 
 // Probabilities (bf16, times v's scale) of 32 positions from the products s of codes and
-// queries; moves the running maximum where a logit passes it by more than kSlack.
+// queries; moves the running maximum where a logit passes it by more than kSlack. Masks cost
+// more than the rest together, so a tile takes them only where some row of the wave does not
+// see some position, in branches of their own (kept from being turned into selects).
 template <int D, int R>
 __device__ __forceinline__ void probabilities(State<D, R>& st, bf16x8 (&p)[R], const f32x4 (&s)[R][2], const Affine& af,
                                               const float (&zq)[R], const Sight<R>& sg) {
     const int qd = (threadIdx.x & 63) >> 4;
-    // whether any of the wave's rows does not see any of the 32 positions
     const bool edge = sg.known[0] < 16 || sg.known[1] < 16 || sg.at + 31 > sg.first_last;
+    const auto seen = [&](int r, int u, int i) {
+        return qd * 4 + i < sg.known[u] && sg.at + u * 16 + qd * 4 + i <= sg.last[r];
+    };
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        bool seen[2][4];
-        if (edge) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) seen[u][i] = qd * 4 + i < sg.known[u] && sg.at + u * 16 + qd * 4 + i <= sg.last[r];
-        }
         float y[2][4];
-        float top = -INFINITY;
+        const auto hide = [&]() {
+            if (edge) {
+                asm volatile("");
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[u][i] = seen(r, u, i) ? y[u][i] : -INFINITY;
+            }
+        };
         const float base = kLift - st.m[r];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                y[u][i] = fmaf(af.ks[u][i], s[r][u][i], fmaf(af.kz[u][i], zq[r], base));
-                if (edge) y[u][i] = seen[u][i] ? y[u][i] : -INFINITY;
-                top = fmaxf(top, y[u][i]);
-            }
-        if (__any(top > kLift + kSlack)) {
+            for (int i = 0; i < 4; ++i) y[u][i] = fmaf(af.ks[u][i], s[r][u][i], fmaf(af.kz[u][i], zq[r], base));
+        hide();
+        const auto greatest = [&]() {
+            float top = fmaxf(y[0][0], y[0][1]);
+#pragma unroll
+            for (int k = 2; k < 8; ++k) top = fmaxf(top, y[k >> 2][k & 3]);
+            return top;
+        };
+        if (__any(greatest() > kLift + kSlack)) {
             // the maximum moves: the logits again, without the old one
-            top = kLowest;
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    y[u][i] = fmaf(af.ks[u][i], s[r][u][i], af.kz[u][i] * zq[r]);
-                    if (edge) y[u][i] = seen[u][i] ? y[u][i] : -INFINITY;
-                    top = fmaxf(top, y[u][i]);
-                }
-            const float m = fmaxf(st.m[r], max_over_quads(top));
+                for (int i = 0; i < 4; ++i) y[u][i] = fmaf(af.ks[u][i], s[r][u][i], af.kz[u][i] * zq[r]);
+            hide();
+            const float m = fmaxf(st.m[r], max_over_quads(greatest()));
             const float down = __builtin_amdgcn_exp2f(st.m[r] - m);
             st.m[r] = m;
             st.l[r] *= down;
@@ -238,17 +242,30 @@ __device__ __forceinline__ void probabilities(State<D, R>& st, bf16x8 (&p)[R], c
         for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float e = __builtin_amdgcn_exp2f(y[u][i]);
-                st.l[r] += e;
-                float es = e * af.vs[u][i], ez = af.vz[u][i];
-                if (edge) {
-                    // a slot that is not seen may hold anything
-                    es = seen[u][i] ? es : 0.0f;
-                    ez = seen[u][i] ? ez : 0.0f;
-                }
-                st.z[r] = fmaf(e, ez, st.z[r]);
-                p[r][u * 4 + i] = (__bf16)es;
+                y[u][i] = __builtin_amdgcn_exp2f(y[u][i]);
+                st.l[r] += y[u][i];
             }
+        if (edge) {
+            asm volatile("");
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // what a row does not see may be NaN
+                    const bool sees = seen(r, u, i);
+                    p[r][u * 4 + i] = (__bf16)(sees ? y[u][i] * af.vs[u][i] : 0.0f);
+                    st.z[r] = fmaf(y[u][i], sees ? af.vz[u][i] : 0.0f, st.z[r]);
+                }
+        } else {
+            asm volatile("");
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    p[r][u * 4 + i] = (__bf16)(y[u][i] * af.vs[u][i]);
+                    st.z[r] = fmaf(y[u][i], af.vz[u][i], st.z[r]);
+                }
+        }
     }
 }
 
