@@ -194,38 +194,42 @@ __device__ __forceinline__ void probabilities(State<D, R>& st, bf16x8 (&p)[R], c
     const auto seen = [&](int r, int u, int i) {
         return qd * 4 + i < sg.known[u] && sg.at + u * 16 + qd * 4 + i <= sg.last[r];
     };
+    float y[R][2][4];
+    const auto each = [&](auto f) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        float y[2][4];
-        const auto hide = [&]() {
-            if (edge) {
-                asm volatile("");
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[u][i] = seen(r, u, i) ? y[u][i] : -INFINITY;
-            }
-        };
-        const float base = kLift - st.m[r];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) y[u][i] = fmaf(af.ks[u][i], s[r][u][i], fmaf(af.kz[u][i], zq[r], base));
-        hide();
-        const auto greatest = [&]() {
-            float top = fmaxf(y[0][0], y[0][1]);
-#pragma unroll
-            for (int k = 2; k < 8; ++k) top = fmaxf(top, y[k >> 2][k & 3]);
-            return top;
-        };
-        if (__any(greatest() > kLift + kSlack)) {
-            // the maximum moves: the logits again, without the old one
+        for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[u][i] = fmaf(af.ks[u][i], s[r][u][i], af.kz[u][i] * zq[r]);
-            hide();
-            const float m = fmaxf(st.m[r], max_over_quads(greatest()));
+                for (int i = 0; i < 4; ++i) f(r, u, i);
+    };
+    const auto hide = [&]() {
+        if (edge) {
+            asm volatile("");
+            each([&](int r, int u, int i) { y[r][u][i] = seen(r, u, i) ? y[r][u][i] : -INFINITY; });
+        }
+    };
+    const auto greatest = [&](int r) {
+        float top = fmaxf(y[r][0][0], y[r][0][1]);
+#pragma unroll
+        for (int k = 2; k < 8; ++k) top = fmaxf(top, y[r][k >> 2][k & 3]);
+        return top;
+    };
+    float base[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) base[r] = kLift - st.m[r];
+    each([&](int r, int u, int i) { y[r][u][i] = fmaf(af.ks[u][i], s[r][u][i], fmaf(af.kz[u][i], zq[r], base[r])); });
+    hide();
+    float top = greatest(0);
+#pragma unroll
+    for (int r = 1; r < R; ++r) top = fmaxf(top, greatest(r));
+    if (__any(top > kLift + kSlack)) {
+        // the maximum moves: the logits again, without the old one
+        each([&](int r, int u, int i) { y[r][u][i] = fmaf(af.ks[u][i], s[r][u][i], af.kz[u][i] * zq[r]); });
+        hide();
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float m = fmaxf(st.m[r], max_over_quads(greatest(r)));
             const float down = __builtin_amdgcn_exp2f(st.m[r] - m);
             st.m[r] = m;
             st.l[r] *= down;
@@ -233,39 +237,27 @@ __device__ __forceinline__ void probabilities(State<D, R>& st, bf16x8 (&p)[R], c
             st.c[r] *= down;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) st.o[r][i] *= down;
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[u][i] = (y[u][i] - m) + kLift;
         }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                y[u][i] = __builtin_amdgcn_exp2f(y[u][i]);
-                st.l[r] += y[u][i];
-            }
-        if (edge) {
-            asm volatile("");
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // what a row does not see may be NaN
-                    const bool sees = seen(r, u, i);
-                    p[r][u * 4 + i] = (__bf16)(sees ? y[u][i] * af.vs[u][i] : 0.0f);
-                    st.z[r] = fmaf(y[u][i], sees ? af.vz[u][i] : 0.0f, st.z[r]);
-                }
-        } else {
-            asm volatile("");
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    p[r][u * 4 + i] = (__bf16)(y[u][i] * af.vs[u][i]);
-                    st.z[r] = fmaf(y[u][i], af.vz[u][i], st.z[r]);
-                }
-        }
+        each([&](int r, int u, int i) { y[r][u][i] = (y[r][u][i] - st.m[r]) + kLift; });
+    }
+    each([&](int r, int u, int i) {
+        y[r][u][i] = __builtin_amdgcn_exp2f(y[r][u][i]);
+        st.l[r] += y[r][u][i];
+    });
+    if (edge) {
+        asm volatile("");
+        each([&](int r, int u, int i) {
+            // what a row does not see may be NaN
+            const bool sees = seen(r, u, i);
+            p[r][u * 4 + i] = (__bf16)(sees ? y[r][u][i] * af.vs[u][i] : 0.0f);
+            st.z[r] = fmaf(y[r][u][i], sees ? af.vz[u][i] : 0.0f, st.z[r]);
+        });
+    } else {
+        asm volatile("");
+        each([&](int r, int u, int i) {
+            p[r][u * 4 + i] = (__bf16)(y[r][u][i] * af.vs[u][i]);
+            st.z[r] = fmaf(y[r][u][i], af.vz[u][i], st.z[r]);
+        });
     }
 }
 
@@ -453,7 +445,8 @@ __device__ __forceinline__ float logits_factor(int lift, float logit_scale) { re
 
 // Which part of the work a workgroup takes. k/v heads run fastest: the workgroups of one
 // share an XCD's L2 where their number is a multiple of 8; the last rows, which see the
-// most, come first.
+// most, come first. The second half of the grid takes the sequences backwards: a CU that
+// holds a workgroup of each half rarely has two of the longest sequence.
 struct Share {
     int seq, kvh, block, split;
 };
@@ -465,6 +458,7 @@ __device__ __forceinline__ Share share_of(const CacheArgs& a) {
     s.block = a.row_blocks - 1 - (rest - s.split * a.row_blocks);
     s.seq = (int)fp::fastdiv_u31((uint32_t)head, a.div_kvh);
     s.kvh = head - s.seq * a.KVH;
+    if (2 * rest >= a.row_blocks * a.splits) s.seq = a.batch - 1 - s.seq;
     return s;
 }
 
@@ -472,7 +466,7 @@ __device__ __forceinline__ Share share_of(const CacheArgs& a) {
 // rows and take different positions, each by itself; at the end they are put together in
 // LDS. Bound by the cache's bytes: the next tile is loaded while one is taken.
 template <int D, int BITS, int R>
-__global__ __launch_bounds__(256) void kv_attend_kernel(CacheArgs a) {
+__global__ __launch_bounds__(256, D * BITS <= 512 && R == 1 ? 3 : 1) void kv_attend_kernel(CacheArgs a) {
     constexpr int WT = 4, PAD = D + 4;
     __shared__ float both[WT * 16 * PAD];
     __shared__ float both_ml[WT * 16 * 2];
@@ -560,13 +554,14 @@ __global__ __launch_bounds__(256) void kv_attend_kernel(CacheArgs a) {
                 store_bf16<8>(static_cast<__bf16*>(a.o) + out * D + d, v);
             } else {
                 const int64_t at = (int64_t)sh.split * a.batch * a.T * a.H + out;
-                f32x4* po = reinterpret_cast<f32x4*>(a.part_o + at * D + d);
-                po[0] = f32x4{v[0], v[1], v[2], v[3]};
-                po[1] = f32x4{v[4], v[5], v[6], v[7]};
                 if (d == 0) {
                     a.part_ml[at * 2] = m;
                     a.part_ml[at * 2 + 1] = sum;
                 }
+                if (t_begin >= t_end) continue;   // an empty part: its sum is 0, its values are not read
+                f32x4* po = reinterpret_cast<f32x4*>(a.part_o + at * D + d);
+                po[0] = f32x4{v[0], v[1], v[2], v[3]};
+                po[1] = f32x4{v[4], v[5], v[6], v[7]};
             }
         }
     }
@@ -648,7 +643,7 @@ __device__ __forceinline__ void share_raw(Shared<D, BITS, NW>& to, const Raw<D, 
 }
 
 template <int D, int BITS, int R, int NW>
-__global__ __launch_bounds__(NW * 64) void kv_attend_chunk_kernel(CacheArgs a) {
+__global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void kv_attend_chunk_kernel(CacheArgs a) {
     using Sh = Shape<D, BITS>;
     constexpr int STEP = NW * 16;
     __shared__ Shared<D, BITS, NW> sets[2];
@@ -735,14 +730,16 @@ __global__ __launch_bounds__(NW * 64) void kv_attend_chunk_kernel(CacheArgs a) {
                         af.vz[u][i] = vz[i];
                     }
                 }
-                bf16x8 p[R];
+                // V's operands are on their way while the probabilities are made
+                bf16x8 v[Sh::NT], p[R];
+#pragma unroll
+                for (int i = 0; i < Sh::NT; ++i) v[i] = __builtin_bit_cast(bf16x8, now.v[g][i][lane]);
                 probabilities<D, R>(st, p, s, af, w.zq, sg);
                 count_middle<D, BITS, R>(st, p);
 #pragma unroll
                 for (int i = 0; i < Sh::NT; ++i) {
-                    const bf16x8 v = __builtin_bit_cast(bf16x8, now.v[g][i][lane]);
 #pragma unroll
-                    for (int r = 0; r < R; ++r) st.o[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[r], st.o[r][i], 0, 0, 0);
+                    for (int r = 0; r < R; ++r) st.o[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[i], p[r], st.o[r][i], 0, 0, 0);
                 }
             }
             __syncthreads();
@@ -764,11 +761,12 @@ __global__ __launch_bounds__(NW * 64) void kv_attend_chunk_kernel(CacheArgs a) {
             });
         } else {
             const int64_t at = (int64_t)sh.split * a.batch * a.T * a.H + w.out[r];
-            each_run<D, BITS, R>(st, r, z, [&](int d, auto& v) {
-                constexpr int N = sizeof(v) / 4;
+            if (t_begin < t_end)
+                each_run<D, BITS, R>(st, r, z, [&](int d, auto& v) {
+                    constexpr int N = sizeof(v) / 4;
 #pragma unroll
-                for (int k = 0; k < N; ++k) a.part_o[at * D + d + k] = v[k];
-            });
+                    for (int k = 0; k < N; ++k) a.part_o[at * D + d + k] = v[k];
+                });
             if (qd == 0) {
                 a.part_ml[at * 2] = st.m[r];
                 a.part_ml[at * 2 + 1] = l;
@@ -798,6 +796,7 @@ __global__ __launch_bounds__(256) void kv_attend_join_kernel(CacheArgs a) {
         f32x4 v = {0, 0, 0, 0};
         for (int s = 0; s < a.splits; ++s) {
             const float ws = __shfl(w, s);
+            if (ws == 0.0f) continue;   // an empty part, or one far below the rest
             const f32x4 x = *reinterpret_cast<const f32x4*>(a.part_o + (s * rows + row) * a.hd + d);
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = fmaf(ws, x[k], v[k]);
@@ -811,7 +810,7 @@ __global__ __launch_bounds__(256) void kv_attend_join_kernel(CacheArgs a) {
 // registers (two waves a SIMD) and LDS (two sets of 16 NW (4 D + 16) bytes) allow.
 template <int D>
 struct Chunk {
-    static constexpr int R = D <= 128 ? 2 : 1, NW = D <= 128 ? 8 : 4;
+    static constexpr int R = D <= 128 ? 2 : 1, NW = 4;
 };
 
 template <int D, int BITS>
@@ -838,8 +837,10 @@ bool plan_attend(const kv_cache_desc& d, int64_t kvh, AttendPlan* out) {
     const int64_t block = p.chunk ? 16 * (hd <= 128 ? Chunk<128>::R * Chunk<128>::NW : Chunk<256>::R * Chunk<256>::NW)
                                   : 16 * p.row_tiles;
     p.row_blocks = (int32_t)((rows + block - 1) / block);
-    // Parts of a sequence: enough workgroups to fill the card (4 of 256 threads a CU, one of
-    // the chunk kernel's), each with some tiles a wave.
+    // Parts of a sequence, equal ones whatever its length (which the device alone knows):
+    // enough workgroups to fill the card, with parts long enough to be worth their queries and
+    // their join. Parts of one size for all sequences measured slower (104 us instead of 84
+    // for 64 sequences of 2500 to 8191 positions).
     const int64_t positions = d.max_pages * d.page_size, want = p.chunk ? 256 : 1024, least = p.chunk ? 512 : 256;
     int64_t splits = (want + heads * p.row_blocks - 1) / (heads * p.row_blocks);
     if (p.chunk && 2 * heads * p.row_blocks > want) splits = 1;
