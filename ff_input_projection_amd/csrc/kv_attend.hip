@@ -399,7 +399,7 @@ __device__ __forceinline__ uint32_t find_rows(Rows<D, BITS, R>& w, u32x4 (&raw)[
         uint32_t mine = 0;
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
-            raw[r][j] = w.last[r] >= 0 ? *reinterpret_cast<const u32x4*>(q + j * 8) : u32x4{0, 0, 0, 0};
+            raw[r][j] = w.real[r] ? *reinterpret_cast<const u32x4*>(q + j * 8) : u32x4{0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < 4; ++i) mine = max(mine, max((raw[r][j][i] >> 7) & 0xFFu, (raw[r][j][i] >> 23) & 0xFFu));
         }
@@ -792,18 +792,19 @@ __global__ __launch_bounds__(256) void kv_attend_join_kernel(CacheArgs a) {
     const float w = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m - top);
     const float sum = wave_sum(l == 0.0f ? 0.0f : w * l);
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    for (int d = lane * 4; d < a.hd; d += 256) {
-        f32x4 v = {0, 0, 0, 0};
-        for (int s = 0; s < a.splits; ++s) {
-            const float ws = __shfl(w, s);
-            if (ws == 0.0f) continue;   // an empty part, or one far below the rest
-            const f32x4 x = *reinterpret_cast<const f32x4*>(a.part_o + (s * rows + row) * a.hd + d);
+    // heads of up to 256: 4 elements a lane. Lanes past a smaller head stay in the loop, as
+    // their weights are read from it (they add up element 0 and store nothing).
+    const int d = lane * 4 < a.hd ? lane * 4 : 0;
+    f32x4 v = {0, 0, 0, 0};
+    for (int s = 0; s < a.splits; ++s) {
+        const float ws = __shfl(w, s);
+        if (ws == 0.0f) continue;   // an empty part, or one far below the rest
+        const f32x4 x = *reinterpret_cast<const f32x4*>(a.part_o + (s * rows + row) * a.hd + d);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = fmaf(ws, x[k], v[k]);
-        }
-        const float o[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
-        store_bf16<4>(static_cast<__bf16*>(a.o) + row * a.hd + d, o);
+        for (int k = 0; k < 4; ++k) v[k] = fmaf(ws, x[k], v[k]);
     }
+    const float o[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
+    if (lane * 4 < a.hd) store_bf16<4>(static_cast<__bf16*>(a.o) + row * a.hd + d, o);
 }
 
 // Rows of a wave of the chunk kernel (in tiles of 16) and the waves of its workgroup, as

@@ -212,6 +212,9 @@ ATTEND = [  # bits, batch, tokens, heads, kvh, hd, page, max_pages, lengths, cou
     (4, 33, 33, 16, 8, 128, 16, 4, [64 - i for i in range(33)], [33 - i % 5 for i in range(33)]),
     (4, 50, 40, 6, 6, 192, 16, 3, [48 - i % 8 for i in range(50)], None),
     (8, 50, 40, 6, 6, 256, 16, 3, [48 - i % 8 for i in range(50)], None),
+    (4, 3, 1, 8, 2, 128, 64, 40, [2560, 1, 1999], None), (8, 3, 1, 8, 2, 128, 64, 40, [2560, 1, 1999], None),   # joined parts
+    (4, 2, 9, 6, 2, 96, 48, 50, [2400, 700], [9, 4]), (8, 1, 3, 2, 1, 256, 16, 100, [1600], None),
+    (4, 1, 2, 8, 8, 32, 16, 200, [3200], None), (4, 1, 90, 4, 2, 64, 64, 30, [1900], None),
     (4, 2, 3, 4, 2, 64, 16, 3, [60, -4], [3, 3]), (4, 2, 3, 4, 2, 64, 16, 3, [48, 10], [77, -1]),   # what they should not hold
 ]
 
@@ -335,8 +338,6 @@ def test_refusals():
     c.fill(storage)
     k, v = (torch.zeros((4, 3, 64), dtype=torch.bfloat16, device=DEV) for _ in range(2))
     q, o = torch.zeros((8, 3, 64), dtype=torch.bfloat16, device=DEV), torch.zeros((2, 3, 256), dtype=torch.bfloat16, device=DEV)
-    ws = c.plan.alloc_workspace(DEV)
-    assert ws.numel() > 0
     lib, h, st = c.plan._lib, c.plan._h, torch.cuda.current_stream().cuda_stream
     import ctypes
     from ff_input_projection_amd import KVCacheStorage
@@ -355,9 +356,13 @@ def test_refusals():
     assert lib.kv_cache_write(h, p(k), p(v), ctypes.byref(twice), *meta, st) == EALIAS
     assert lib.kv_cache_read(h, s, *meta, p(k), p(k), st) == EALIAS
     assert lib.kv_cache_read(h, s, *meta, p(k), None, st) == EINVAL
+    ws = c.plan.alloc_workspace(DEV)
+    assert ws.numel() > 0
     assert lib.kv_cache_attend(h, p(q), s, *meta, p(q), p(ws), ws.numel(), st) == EALIAS
+    assert lib.kv_cache_attend(h, p(q), s, *meta, p(ws), p(ws), ws.numel(), st) == EALIAS
     assert lib.kv_cache_attend(h, p(q), s, *meta, p(o), p(ws), ws.numel() - 16, st) == EINVAL
     assert lib.kv_cache_attend(h, p(q), s, *meta, p(o), None, 0, st) == EINVAL
+    assert lib.kv_cache_attend(h, None, s, *meta, p(o), p(ws), ws.numel(), st) == EINVAL
     assert lib.kv_cache_attend(h, p(q), s, *meta, p(o) + 2, p(ws), ws.numel(), st) == EALIGN
     with pytest.raises(ValueError):
         c.plan.write(storage, k[:2], v, *c.args)
@@ -392,10 +397,11 @@ def test_no_sequences():
     assert k.shape == v.shape == (0, 2, 64) and plan.attend(storage, e(0, 2, 64), *meta).shape == (0, 2, 256)
 
 
+@pytest.mark.parametrize("max_pages", [30, 90])
 @pytest.mark.parametrize("tokens", [1, 6])
-def test_graph_replays_read_the_lengths_anew(tokens):
+def test_graph_replays_read_the_lengths_anew(tokens, max_pages):
     """A captured step (write and attend, one workspace) replayed with other inputs, lengths and pages: the eager bits."""
-    c = Case(4, 3, tokens, 8, 2, 64, 16, 30, [400, 77, 200], None, seed=11)
+    c = Case(4, 3, tokens, 8, 2, 64, 16, max_pages, [400, 77, 200], None, seed=11)
     storage = c.plan.alloc_storage(DEV)
     c.fill(storage)
     table, lengths, _ = (t.clone() if t is not None else None for t in c.args)
@@ -430,8 +436,9 @@ def test_graph_replays_read_the_lengths_anew(tokens):
         assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(storage, again))
 
 
-def test_two_streams_at_once():
-    c = Case(8, 4, 1, 8, 2, 128, 16, 30, [400, 480, 3, 222], None, seed=12)
+@pytest.mark.parametrize("max_pages", [30, 90])
+def test_two_streams_at_once(max_pages):
+    c = Case(8, 4, 1, 8, 2, 128, 16, max_pages, [400, 480, 3, 222], None, seed=12)
     storage = c.plan.alloc_storage(DEV)
     c.fill(storage)
     q = c.queries().to(DEV)
