@@ -847,6 +847,7 @@ bool plan_attend(const kv_cache_desc& d, int64_t kvh, AttendPlan* out) {
     if (p.chunk && 2 * heads * p.row_blocks > want) splits = 1;
     if (splits > (positions + least - 1) / least) splits = (positions + least - 1) / least;
     p.splits = (int32_t)(splits < 1 ? 1 : splits > 64 ? 64 : splits);
+    if (heads * p.row_blocks * p.splits > (int64_t(1) << 23)) return false;   // of 256 threads: one grid
     if (p.splits > 1) p.workspace = (size_t)p.splits * (size_t)(d.batch * d.tokens * d.n_heads) * (size_t)(hd + 2) * 4;
     *out = p;
     return true;

@@ -55,7 +55,7 @@ struct AttendPlan {
     int32_t row_blocks = 0, splits = 0;
     size_t workspace = 0;
 };
-bool plan_attend(const kv_cache_desc& d, int64_t kvh, AttendPlan* out);   // false: head_dim not supported
+bool plan_attend(const kv_cache_desc& d, int64_t kvh, AttendPlan* out);   // false: not supported
 hipError_t launch_attend(const kv_cache_desc& d, const AttendPlan& p, const CacheArgs& a, hipStream_t st);
 
 }  // namespace fp

@@ -23,8 +23,9 @@ using fp::CacheArgs;
 // Where a row of the step lies in the cache: its row index, or -1 for none.
 __device__ __forceinline__ int64_t slot_of(const CacheArgs& a, int seq, int head, int s) {
     const fp::Step st = fp::step_of(a, seq);
+    if (s >= st.count) return -1;
     const int32_t p = st.first + s;
-    if (s >= st.count || p < 0 || p >= a.capacity) return -1;
+    if (p < 0 || p >= a.capacity) return -1;
     const int32_t pg = (int32_t)fp::fastdiv_u31((uint32_t)p, a.div_page);
     const int32_t page = a.table[(int64_t)seq * a.max_pages + pg];
     if (page < 0 || page >= a.n_pages) return -1;
@@ -205,14 +206,14 @@ int check(const kv_cache_desc* d, Derived* out) {
     if (d->dtype != FUSED_PROJ_BF16) return FUSED_PROJ_EUNSUPPORTED;
     if (d->head_dim % 8 != 0 || d->head_dim > 512) return FUSED_PROJ_EUNSUPPORTED;
     if (d->page_size % 16 != 0 || d->page_size > 65536) return FUSED_PROJ_EUNSUPPORTED;
-    if (d->n_pages > kMaxIndex || d->max_pages > kMaxIndex || d->max_pages * d->page_size > kMaxIndex)
+    if (d->n_pages > kMaxIndex || d->max_pages > kMaxIndex || d->max_pages * d->page_size > kMaxIndex / 2)
         return FUSED_PROJ_EUNSUPPORTED;
     Derived r;
     r.kvh = d->n_kv_heads > 0 ? d->n_kv_heads : d->n_heads;
     r.q_rows = mul_cap(mul_cap(d->batch, d->tokens), d->n_heads);
     if (d->n_heads > kMaxIndex || d->tokens > kMaxIndex || d->batch > kMaxIndex || r.q_rows < 0 || r.q_rows > kMaxIndex)
         return FUSED_PROJ_EUNSUPPORTED;
-    if (mul_cap(d->n_heads, d->tokens) > kMaxIndex || mul_cap(d->batch, d->max_pages) < 0) return FUSED_PROJ_EUNSUPPORTED;
+    if (mul_cap(d->n_heads, d->tokens) > kMaxIndex / 2 || mul_cap(d->batch, d->max_pages) < 0) return FUSED_PROJ_EUNSUPPORTED;
     r.rows = d->batch * r.kvh * d->tokens;
     const int64_t slots = mul_cap(mul_cap(d->n_pages, r.kvh), d->page_size);
     r.codes = mul_cap(slots, d->head_dim * d->bits / 8);
@@ -220,6 +221,7 @@ int check(const kv_cache_desc* d, Derived* out) {
     if (slots < 0 || r.codes < 0 || r.params < 0) return FUSED_PROJ_EUNSUPPORTED;
     r.lpr = 1;
     while (r.lpr * 8 < d->head_dim) r.lpr *= 2;
+    if (r.rows * r.lpr > kMaxIndex) return FUSED_PROJ_EUNSUPPORTED;   // threads of one grid
     if (out) *out = r;
     return FUSED_PROJ_OK;
 }

@@ -129,53 +129,70 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void layer_norm_rows_kernel(
     }
 }
 
+// As for the strips below, the registers of a row's pieces take the next row's as its dx is
+// written, and nothing else is loaded in between.
 template <typename T, int NCH, int TPR, bool TAIL>
 __global__ __launch_bounds__(TPR < 512 ? 512 : TPR) void layer_norm_rows_grad_kernel(NormArgs a) {
     constexpr int V = Piece<T>::V, BLOCK = TPR < 512 ? 512 : TPR, RPB = BLOCK / TPR, WPR = TPR / 64;
     __shared__ float red[BLOCK / 64 * 2];
     __shared__ float both[RPB > 1 ? 2 * NCH * TPR * V : 1];
+    constexpr bool kAhead = TPR < 1024;   // a workgroup of 1024 has too few registers for it
     const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     const auto whole = [](int i) { return !TAIL || (TPR < 1024 && i < NCH - 1); };
-    const T* gamma = static_cast<const T*>(a.gamma);
+    const auto left = [&](int i) { return a.C - (i * TPR + lane) * V; };   // values of the row from the piece on
+    const auto inside = [&](int i) { return (TPR < 1024 && i < NCH - 1) || left(i) > 0; };
+    u32x4 hx[NCH], hd[NCH], hg[NCH];
     float dg[NCH][V], db[NCH][V];
 #pragma unroll
-    for (int i = 0; i < NCH; ++i)
+    for (int i = 0; i < NCH; ++i) {
+        hg[i] = inside(i) ? load_piece(static_cast<const T*>(a.gamma) + (i * TPR + lane) * V, left(i), whole(i)) : u32x4{0, 0, 0, 0};
 #pragma unroll
         for (int e = 0; e < V; ++e) dg[i][e] = db[i][e] = 0.0f;
-    // every row slot of the workgroup takes the same number of turns, so that its barriers meet
-    for (int first = blockIdx.x * RPB; first < a.M; first += gridDim.x * RPB) {
-        const int row = first + sub;
-        const bool real = row < a.M;
-        const T* x = row_of<T>(a, real ? row : 0);
-        const T* dy = static_cast<const T*>(a.dy) + (int64_t)(real ? row : 0) * a.C;
-        const float mean = a.mean[real ? row : 0], rstd = a.rstd[real ? row : 0];
-        u32x4 hx[NCH], hd[NCH];
+    }
+    const T* x;
+    const T* dy;
+    float mean_next = 0.0f, rstd_next = 0.0f;
+    const auto go_to = [&](int row) {
+        x = row_of<T>(a, row);
+        dy = static_cast<const T*>(a.dy) + (int64_t)row * a.C;
+        mean_next = a.mean[row];
+        rstd_next = a.rstd[row];
+    };
+    const auto load = [&](int i) {
+        hx[i] = load_piece(x + (i * TPR + lane) * V, left(i), whole(i));
+        hd[i] = load_piece(dy + (i * TPR + lane) * V, left(i), whole(i));
+    };
+    const int row0 = blockIdx.x * RPB + sub, turn = gridDim.x * RPB;
+    if (row0 < a.M) go_to(row0);
 #pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-            const int c = (i * TPR + lane) * V, n = a.C - c;
-            hx[i] = hd[i] = u32x4{0, 0, 0, 0};
-            if (real && n > 0) {
-                hx[i] = load_piece(x + c, n, whole(i));
-                hd[i] = load_piece(dy + c, n, whole(i));
-            }
-        }
+    for (int i = 0; i < NCH; ++i) {
+        hx[i] = hd[i] = u32x4{0, 0, 0, 0};
+        if (row0 < a.M && inside(i)) load(i);
+    }
+    // every row slot of the workgroup takes the same number of turns, so that its barriers meet
+    for (int row = row0; row - sub < a.M; row += turn) {
+        const bool real = row < a.M;
+        const float mean = mean_next, rstd = rstd_next;
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-            const int c = (i * TPR + lane) * V, n = a.C - c;
-            if (real && n > 0) {
-                const u32x4 g = load_piece(gamma + c, n, whole(i));
+            if (real && inside(i)) {
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    if (whole(i) || e < n) {
+                    if (whole(i) || e < left(i)) {
                         const float d = Piece<T>::get(hd[i], e), xh = (Piece<T>::get(hx[i], e) - mean) * rstd;
-                        const float gd = d * Piece<T>::get(g, e);
+                        const float gd = d * Piece<T>::get(hg[i], e);
                         s1 += gd;
                         s2 = fmaf(gd, xh, s2);
                         dg[i][e] = fmaf(d, xh, dg[i][e]);
                         db[i][e] += d;
                     }
                 }
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                settle(dg[i][e]);
+                settle(db[i][e]);
             }
         }
         s1 = wave_sum(s1);
@@ -195,24 +212,29 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR) void layer_norm_rows_grad_ke
             }
             __syncthreads();
         }
-        s1 *= a.inv_c;
-        s2 *= a.inv_c;
+        // dx = rstd (d gamma - c1 - xhat c2) = d gamma rstd + (x - mean) t2 + t1
+        const float t1 = -rstd * (s1 * a.inv_c), t2 = -rstd * (rstd * (s2 * a.inv_c));
         T* dx = static_cast<T*>(a.y) + (int64_t)row * a.C;
+        const bool more = row + turn < a.M;
+        if (more) go_to(row + turn);
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-            const int c = (i * TPR + lane) * V, n = a.C - c;
             unpack_again(hx[i]);
             unpack_again(hd[i]);
-            if (real && n > 0) {
-                const u32x4 g = load_piece(gamma + c, n, whole(i));
+            if (real && inside(i)) {
                 float o[V];
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float xh = (Piece<T>::get(hx[i], e) - mean) * rstd;
-                    o[e] = rstd * (fmaf(Piece<T>::get(hd[i], e), Piece<T>::get(g, e), -s1) - xh * s2);
-                }
-                store_piece<T>(dx + c, o, n, whole(i));
+                for (int e = 0; e < V; ++e)
+                    o[e] = fmaf(Piece<T>::get(hx[i], e) - mean, t2, fmaf(Piece<T>::get(hd[i], e) * Piece<T>::get(hg[i], e), rstd, t1));
+                store_piece<T>(dx + (i * TPR + lane) * V, o, left(i), whole(i));
+                if (kAhead && more) load(i);
             }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (!kAhead && more) {
+#pragma unroll
+            for (int i = 0; i < NCH; ++i)
+                if (inside(i)) load(i);
         }
     }
     // the workgroup's sums: its row slots add theirs in turn
@@ -338,8 +360,10 @@ __global__ __launch_bounds__(NT) void layer_norm_strips_kernel(NormArgs a) {
     __shared__ float red[NT / 64 * TT];
     __shared__ float tot[2][TT];
     const int tl = threadIdx.x % TL, cr = threadIdx.x / TL;
+    const uint32_t bid = blockIdx.y * gridDim.x + blockIdx.x;   // rows of kMostBlocks
+    if (bid >= (uint32_t)a.all_strips) return;
     int bi, first, twice;
-    strip_tokens<TT, EDGE>(a, strip_of(blockIdx.x, gridDim.x), bi, first, twice);
+    strip_tokens<TT, EDGE>(a, strip_of((int)bid, a.all_strips), bi, first, twice);
     const int n = EDGE ? a.S - first - tl * V : V;
     const int nch = NCH > 0 ? NCH : (a.C + R - 1) / R;
     const T* x = static_cast<const T*>(a.x) + (int64_t)bi * a.x_sb + first;
@@ -613,6 +637,7 @@ __global__ __launch_bounds__(1024) void layer_norm_columns_kernel(const float* p
 
 // ------------------------------------------------------------------ plans
 constexpr int64_t kMaxIndex = (int64_t(1) << 31) - 1;
+constexpr int kMostBlocks = 1 << 20;   // along a grid's dimension, of up to 1024 threads: fewer than 2^32
 
 struct Derived {
     int64_t S = 0, M = 0, C = 0, sb = 0, ss = 0, sc = 0, x_span = 0;
@@ -765,15 +790,16 @@ NormArgs base_args(const layer_norm_plan* h, const void* x, const void* gamma, i
     return a;
 }
 
-void launch(void (*kernel)(NormArgs), unsigned grid, int block, const NormArgs& a, hipStream_t st) {
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), 0, st, a);
+void launch(void (*kernel)(NormArgs), int64_t grid, int block, const NormArgs& a, hipStream_t st) {
+    const unsigned x = (unsigned)(grid < kMostBlocks ? grid : kMostBlocks), y = (unsigned)((grid + x - 1) / x);
+    hipLaunchKernelGGL(kernel, dim3(x, y), dim3(block), 0, st, a);
 }
 
 template <typename T, bool TAIL>
 void launch_rows(const Derived& r, const NormArgs& a, bool grad, hipStream_t st) {
     const int tpr = grad ? r.g_tpr : r.tpr, nch = grad ? r.g_nch : r.nch;
     const int block = tpr < (grad ? 512 : 256) ? (grad ? 512 : 256) : tpr, rpb = block / tpr;
-    const unsigned grid = grad ? (unsigned)r.parts : (unsigned)((r.M + rpb - 1) / rpb);
+    const int64_t want = (r.M + rpb - 1) / rpb, grid = grad ? r.parts : want < kMostBlocks ? want : kMostBlocks;
 #define LN_CASE(N, TPR)                                                                         \
     if (tpr == TPR && nch == N)                                                                 \
         return launch(grad ? layer_norm_rows_grad_kernel<T, N, TPR, TAIL> : layer_norm_rows_kernel<T, N, TPR, TAIL>, \
@@ -787,7 +813,7 @@ void launch_rows(const Derived& r, const NormArgs& a, bool grad, hipStream_t st)
 
 template <typename T>
 void launch_strips(const Derived& r, const NormArgs& a, bool grad, hipStream_t st) {
-    const unsigned grid = grad ? (unsigned)r.parts : (unsigned)a.all_strips;
+    const int64_t grid = grad ? r.parts : a.all_strips;
     const bool shift = r.S % (4 * Piece<T>::V) != 0;
     if (r.edge)
         return launch(grad ? layer_norm_strips_grad_kernel<T, 0, 4, 1024, false, true> : layer_norm_strips_kernel<T, 0, 4, 1024, true>,

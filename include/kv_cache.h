@@ -85,8 +85,9 @@ typedef struct kv_cache_storage {
 
 /* Host-only check. FUSED_PROJ_OK, FUSED_PROJ_EINVAL (malformed: sizes, enums, KVH not
  * dividing H, a negative or non-finite sm_scale) or FUSED_PROJ_EUNSUPPORTED (not bf16,
- * head_dim or page_size outside the ranges above, max_pages page_size or b T H above
- * 2^31 - 1, a tensor of 2^60 bytes). */
+ * head_dim or page_size outside the ranges above, max_pages page_size or T H of 2^30 or
+ * more, b T H or b T KVH times head_dim / 8 (rounded up to a power of two) of 2^31 or more,
+ * storage of 2^60 bytes or more). */
 int kv_cache_validate(const kv_cache_desc *desc);
 
 /* Validates and fixes the split of the work; touches no GPU memory. Errors: as validate,
@@ -121,7 +122,8 @@ int kv_cache_attend_workspace_size(kv_cache_t plan, size_t *bytes);
  * output reads). The step's own k and v are in the cache already. workspace: device, at
  * least kv_cache_attend_workspace_size bytes, contents do not matter; calls that share it
  * must not overlap in time. Errors as kv_cache_write, and FUSED_PROJ_EUNSUPPORTED for a
- * head_dim that attention does not take, FUSED_PROJ_EINVAL for a short workspace. */
+ * head_dim that attention does not take (or 2^23 workgroups or more), FUSED_PROJ_EINVAL for
+ * a short workspace. */
 int kv_cache_attend(kv_cache_t plan, const void *q, const kv_cache_storage *storage, const int32_t *table,
                     const int32_t *lengths, const int32_t *counts, void *o, void *workspace, size_t workspace_bytes,
                     void *stream);

@@ -344,3 +344,36 @@ def test_norm_and_projection_in_training(layout):
     for name, got, want in [("ff", ff, parts[0].detach()), ("q", q, parts[1].detach()), ("dx", dx, x64.grad),
                             ("dgamma", dgamma, g64.grad), ("dbeta", dbeta, b64.grad), ("dw", dw, w64.grad)]:
         check(name, got, want, torch.full_like(want, 2000 * U * want.abs().max().item()))
+
+
+@pytest.mark.parametrize("layout", ["tokens_last", "channels_first"])
+def test_more_tokens_than_one_dimension_of_a_grid(layout):
+    """1.2 million slabs of one token, and 5 million tokens: more workgroups than a grid's dimension takes at once."""
+    batch, tokens = (1_200_000, 1) if layout == "channels_first" else (1, 5_000_000)
+    shape = (batch, 8, tokens) if layout == "channels_first" else (batch, tokens, 8)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x, dy = (torch.randn(shape, generator=g, device=DEV) for _ in range(2))
+    gamma, beta = torch.linspace(0.5, 1.5, 8, device=DEV), torch.linspace(-1.0, 1.0, 8, device=DEV)
+    ln = LayerNorm.for_tensor(x, layout)
+    y, stats = ln(x, gamma, beta)
+    dx, dgamma, dbeta = ln.backward(x, gamma, stats, dy)
+    torch.cuda.synchronize()
+    axis, wide = (1, [1, 8, 1]) if layout == "channels_first" else (2, [1, 1, 8])
+    x64, d = x.double(), dy.double()
+    mean = x64.mean(axis, keepdim=True)
+    rstd = ((x64 - mean).square().mean(axis, keepdim=True) + 1e-5) ** -0.5
+    xhat, g64 = (x64 - mean) * rstd, gamma.double().view(wide)
+    want = xhat * g64 + beta.double().view(wide)
+    # sums of 8: at most 8 u of the mean magnitude each, and a rounding a step
+    tol = 16 * U * (g64 * (x64.abs().mean(axis, keepdim=True) * rstd + xhat.abs()) + 1.0)
+    assert ((y.double() - want).abs() <= tol).all()
+    gd = d * g64
+    want = rstd * (gd - gd.mean(axis, keepdim=True) - xhat * (gd * xhat).mean(axis, keepdim=True))
+    # x - mean carries 10 u of |x| too, and the given statistics 16 u
+    tol = 40 * U * rstd * (gd.abs() + gd.abs().mean(axis, keepdim=True) + (xhat.abs() + 1 + x64.abs() * rstd)
+                           * (gd * xhat).abs().mean(axis, keepdim=True) * (1 + x64.abs().mean(axis, keepdim=True) * rstd))
+    assert ((dx.double() - want).abs() <= tol).all()
+    other = (0, 2) if layout == "channels_first" else (0, 1)
+    for got, terms in ((dgamma, d * xhat), (dbeta, d)):
+        # up to 5000 additions a thread: their roundings add up to 5000 u of the sum of magnitudes at most
+        assert ((got.double() - terms.sum(other)).abs() <= 6000 * U * (terms.abs() + d.abs()).sum(other)).all()

@@ -50,6 +50,8 @@ def _desc(batch=2, tokens=1, n_heads=8, head_dim=64, **kw):
     (dict(dtype=torch.float32), fpa.EUNSUPPORTED), (dict(head_dim=20), fpa.EUNSUPPORTED),
     (dict(head_dim=520), fpa.EUNSUPPORTED), (dict(page_size=24), fpa.EUNSUPPORTED),
     (dict(page_size=65552), fpa.EUNSUPPORTED), (dict(max_pages=1 << 26, page_size=64), fpa.EUNSUPPORTED),
+    (dict(max_pages=1 << 24, page_size=64), fpa.EUNSUPPORTED), (dict(max_pages=(1 << 24) - 1, page_size=64), fpa.OK),
+    (dict(batch=1 << 14, tokens=1 << 13, head_dim=512), fpa.EUNSUPPORTED), (dict(tokens=1 << 27), fpa.EUNSUPPORTED),
     (dict(max_pages=1 << 62), fpa.EUNSUPPORTED), (dict(batch=1 << 20, tokens=1 << 12), fpa.EUNSUPPORTED),
     (dict(n_pages=(1 << 31) - 1, page_size=65536, n_heads=1 << 20), fpa.EUNSUPPORTED),
 ])
