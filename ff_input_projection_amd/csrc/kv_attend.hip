@@ -642,11 +642,11 @@ __device__ __forceinline__ void share_raw(Shared<D, BITS, NW>& to, const Raw<D, 
     if (lane == 0) to.known[wave] = t.known;
 }
 
-template <int D, int BITS, int R, int NW>
-__global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void kv_attend_chunk_kernel(CacheArgs a) {
+template <int D, int BITS, int R, int NW, int SETS>
+__global__ __launch_bounds__(NW * 64, 2) void kv_attend_chunk_kernel(CacheArgs a) {
     using Sh = Shape<D, BITS>;
     constexpr int STEP = NW * 16;
-    __shared__ Shared<D, BITS, NW> sets[2];
+    __shared__ Shared<D, BITS, NW> sets[SETS];
     __shared__ uint32_t tops[NW];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, qd = lane >> 4;
@@ -692,11 +692,13 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void kv_attend_chunk_ker
         int page = page_of(t_begin + 2);
         __syncthreads();
         for (int turn = t_begin; turn < t_end; ++turn) {
-            const Shared<D, BITS, NW>& now = sets[(turn - t_begin) & 1];
-            // the other set was read before the last barrier
-            if (turn + 1 < t_end) share_raw<D, BITS, NW>(sets[(turn + 1 - t_begin) & 1], raw, wave, c1);
-            load_raw<D, BITS>(raw, a, page, sh.kvh, place(turn + 2), step.length);
-            page = page_of(turn + 3);
+            const Shared<D, BITS, NW>& now = sets[(turn - t_begin) % SETS];
+            const auto prepare_next = [&]() {
+                if (turn + 1 < t_end) share_raw<D, BITS, NW>(sets[(turn + 1 - t_begin) % SETS], raw, wave, c1);
+                load_raw<D, BITS>(raw, a, page, sh.kvh, place(turn + 2), step.length);
+                page = page_of(turn + 3);
+            };
+            if constexpr (SETS == 2) prepare_next();   // the other set was read before the last barrier
 #pragma unroll 1
             for (int g = 0; g < NW / 2; ++g) {
                 Sight<R> sg;
@@ -731,18 +733,24 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void kv_attend_chunk_ker
                     }
                 }
                 // V's operands are on their way while the probabilities are made
-                bf16x8 v[Sh::NT], p[R];
+                constexpr int AHEAD = Sh::NT < 8 ? Sh::NT : 8;
+                bf16x8 v[AHEAD], p[R];
 #pragma unroll
-                for (int i = 0; i < Sh::NT; ++i) v[i] = __builtin_bit_cast(bf16x8, now.v[g][i][lane]);
+                for (int i = 0; i < AHEAD; ++i) v[i] = __builtin_bit_cast(bf16x8, now.v[g][i][lane]);
                 probabilities<D, R>(st, p, s, af, w.zq, sg);
                 count_middle<D, BITS, R>(st, p);
 #pragma unroll
                 for (int i = 0; i < Sh::NT; ++i) {
+                    const bf16x8 x = i < AHEAD ? v[i < AHEAD ? i : 0] : __builtin_bit_cast(bf16x8, now.v[g][i][lane]);
 #pragma unroll
-                    for (int r = 0; r < R; ++r) st.o[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[i], p[r], st.o[r][i], 0, 0, 0);
+                    for (int r = 0; r < R; ++r) st.o[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, p[r], st.o[r][i], 0, 0, 0);
                 }
             }
             __syncthreads();
+            if constexpr (SETS == 1) {
+                prepare_next();
+                __syncthreads();
+            }
         }
     }
 #pragma unroll
@@ -807,17 +815,17 @@ __global__ __launch_bounds__(256) void kv_attend_join_kernel(CacheArgs a) {
     if (lane * 4 < a.hd) store_bf16<4>(static_cast<__bf16*>(a.o) + row * a.hd + d, o);
 }
 
-// Rows of a wave of the chunk kernel (in tiles of 16) and the waves of its workgroup, as
-// registers (two waves a SIMD) and LDS (two sets of 16 NW (4 D + 16) bytes) allow.
-template <int D>
-struct Chunk {
-    static constexpr int R = D <= 128 ? 2 : 1, NW = 4;
-};
+// Rows of a wave of the chunk kernel (in tiles of 16), and sets of operands (of 64 (4 D + 16)
+// bytes each): as two workgroups a CU leave registers and LDS.
+constexpr int kChunkWaves = 4;
+constexpr int chunk_tiles(int64_t d) { return d <= 128 ? 2 : 1; }
+constexpr int chunk_sets(int64_t d) { return d <= 128 ? 2 : 1; }
 
 template <int D, int BITS>
 void launch_shape(const fp::AttendPlan& p, const CacheArgs& a, unsigned grid, hipStream_t st) {
     if (p.chunk)
-        hipLaunchKernelGGL((kv_attend_chunk_kernel<D, BITS, Chunk<D>::R, Chunk<D>::NW>), dim3(grid), dim3(Chunk<D>::NW * 64), 0, st, a);
+        hipLaunchKernelGGL((kv_attend_chunk_kernel<D, BITS, chunk_tiles(D), kChunkWaves, chunk_sets(D)>), dim3(grid),
+                           dim3(kChunkWaves * 64), 0, st, a);
     else if (D > 128 || p.row_tiles == 1)
         hipLaunchKernelGGL((kv_attend_kernel<D, BITS, 1>), dim3(grid), dim3(256), 0, st, a);
     else
@@ -835,16 +843,15 @@ bool plan_attend(const kv_cache_desc& d, int64_t kvh, AttendPlan* out) {
     AttendPlan p;
     p.chunk = rows > 32;
     p.row_tiles = rows <= 16 || hd > 128 ? 1 : 2;   // two tiles of a wider head would spill
-    const int64_t block = p.chunk ? 16 * (hd <= 128 ? Chunk<128>::R * Chunk<128>::NW : Chunk<256>::R * Chunk<256>::NW)
-                                  : 16 * p.row_tiles;
+    const int64_t block = 16 * (p.chunk ? chunk_tiles(hd) * kChunkWaves : p.row_tiles);
     p.row_blocks = (int32_t)((rows + block - 1) / block);
     // Parts of a sequence, equal ones whatever its length (which the device alone knows):
     // enough workgroups to fill the card, with parts long enough to be worth their queries and
     // their join. Parts of one size for all sequences measured slower (104 us instead of 84
     // for 64 sequences of 2500 to 8191 positions).
-    const int64_t positions = d.max_pages * d.page_size, want = p.chunk ? 256 : 1024, least = p.chunk ? 512 : 256;
+    const int64_t positions = d.max_pages * d.page_size, want = p.chunk ? 512 : 1024, least = p.chunk ? 512 : 256;
     int64_t splits = (want + heads * p.row_blocks - 1) / (heads * p.row_blocks);
-    if (p.chunk && 2 * heads * p.row_blocks > want) splits = 1;
+    if (p.chunk && 4 * heads * p.row_blocks > 3 * want) splits = 1;
     if (splits > (positions + least - 1) / least) splits = (positions + least - 1) / least;
     p.splits = (int32_t)(splits < 1 ? 1 : splits > 64 ? 64 : splits);
     if (heads * p.row_blocks * p.splits > (int64_t(1) << 23)) return false;   // of 256 threads: one grid
