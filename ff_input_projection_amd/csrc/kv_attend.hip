@@ -465,8 +465,13 @@ __device__ __forceinline__ Share share_of(const CacheArgs& a) {
 // Few rows (single and drafted tokens): the four waves of a workgroup hold the same R x 16
 // rows and take different positions, each by itself; at the end they are put together in
 // LDS. Bound by the cache's bytes: the next tile is loaded while one is taken.
+//
+// Waves a SIMD: as many as the registers of two tiles and the output leave without spills.
 template <int D, int BITS, int R>
-__global__ __launch_bounds__(256, D * BITS <= 512 && R == 1 ? 3 : 1) void kv_attend_kernel(CacheArgs a) {
+constexpr int kStepWaves = D * BITS > 1536 ? 1 : D * BITS <= 512 && R == 1 && Shape<D, BITS>::D1 == 0 ? 3 : 2;
+
+template <int D, int BITS, int R>
+__global__ __launch_bounds__(256, (kStepWaves<D, BITS, R>)) void kv_attend_kernel(CacheArgs a) {
     constexpr int WT = 4, PAD = D + 4;
     __shared__ float both[WT * 16 * PAD];
     __shared__ float both_ml[WT * 16 * 2];
