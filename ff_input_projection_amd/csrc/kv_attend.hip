@@ -809,12 +809,20 @@ __global__ __launch_bounds__(256) void kv_attend_join_kernel(CacheArgs a) {
     // their weights are read from it (they add up element 0 and store nothing).
     const int d = lane * 4 < a.hd ? lane * 4 : 0;
     f32x4 v = {0, 0, 0, 0};
-    for (int s = 0; s < a.splits; ++s) {
-        const float ws = __shfl(w, s);
-        if (ws == 0.0f) continue;   // an empty part, or one far below the rest
-        const f32x4 x = *reinterpret_cast<const f32x4*>(a.part_o + (s * rows + row) * a.hd + d);
+    for (int s0 = 0; s0 < a.splits; s0 += 4) {   // 4 loads in flight
+        f32x4 x[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = fmaf(ws, x[k], v[k]);
+        for (int k = 0; k < 4; ++k) {
+            const int64_t s = min(s0 + k, a.splits - 1);
+            x[k] = *reinterpret_cast<const f32x4*>(a.part_o + (s * rows + row) * a.hd + d);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float ws = s0 + k < a.splits ? __shfl(w, s0 + k) : 0.0f;
+            // an empty part's values were never written
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = fmaf(ws, ws == 0.0f ? 0.0f : x[k][e], v[e]);
+        }
     }
     const float o[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
     if (lane * 4 < a.hd) store_bf16<4>(static_cast<__bf16*>(a.o) + row * a.hd + d, o);
