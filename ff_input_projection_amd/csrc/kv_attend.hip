@@ -14,7 +14,7 @@
 //   sum_j p_j vhat_j = sum_j b_j (c_j - C) + sum_j p_j (z_j + C s_j),    b_j = p_j s_j in bf16
 // C is the middle code: codes are positive, so the rounding of b_j times c_j would be that of
 // a sum far larger than the result; times c_j - C it is the rounding of the values' own
-// spread (measured: output error 0.0021 of the output's norm instead of 0.0049, of which
+// spread (measured: output error 0.0023 of the output's norm instead of 0.0049, of which
 // 0.0017 is the output's own rounding). C sum_j b_j is one more product, with a constant.
 //
 // Tiles. A wave holds R x 16 query rows (all rows of a k/v head: token by token, its group's
@@ -28,7 +28,7 @@
 //
 // Measured, 4 bits, 32 heads on 8 x 128: 63 sequences of 8191 positions, one token each, 106 us
 // (5.3 TB/s, a large copy's rate; 42% of the vector pipes' time); of 2500 to 8191 positions 83
-// us; 2 x 1024 tokens over 4096 positions 183 us (655 TFLOP/s; a large bf16 product reaches
+// us; 2 x 1024 tokens over 4096 positions 185 us (650 TFLOP/s; a large bf16 product reaches
 // 1209).
 #include <cmath>
 

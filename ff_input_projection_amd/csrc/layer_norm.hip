@@ -276,13 +276,14 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR) void layer_norm_rows_grad_ke
 }
 
 // ------------------------------------------------------------------ channels-first strips
+constexpr int TL = 4;   // lanes along the tokens: 64 bytes of a channel
+
 // A workgroup's strip is TL * V tokens of one slab. Thread (cr, tl) holds V tokens of the
 // channels cr, cr + R, cr + 2R, ... (R = threads / TL).
 //
-// Sum of f[e] over the lanes of a wave with the same tl (lane bits 3..5, and 2 where TL is
-// 4): each exchange halves the values a lane carries, so the sums of 8 values cost 4 + 2 + 1
+// Sum of f[e] over the lanes of a wave with the same tl (lane bits 2..5): each exchange halves the values a lane carries, so the sums of 8 values cost 4 + 2 + 1
 // exchanges instead of 24. The lane's remaining value is the sum for token `lane_token`.
-template <int TL, int V>
+template <int V>
 __device__ __forceinline__ float strip_sum(const float (&f)[V]) {
     float r;
     if constexpr (V == 8) {
@@ -296,10 +297,10 @@ __device__ __forceinline__ float strip_sum(const float (&f)[V]) {
         r = swap_sum16(a0, a1);
         r += dpp<kRowRor8>(r);
     }
-    if constexpr (TL == 4) r += dpp<0x1B>(dpp<kHalfMirror>(r));   // lane ^ 7, then ^ 3: lane ^ 4
+    r += dpp<0x1B>(dpp<kHalfMirror>(r));   // lane ^ 7, then ^ 3: lane ^ 4
     return r;
 }
-template <int TL, int V>
+template <int V>
 __device__ __forceinline__ int lane_token() {
     const int l = threadIdx.x & 63, b5 = l >> 5, b4 = (l >> 4) & 1, b3 = (l >> 3) & 1;
     return (l & (TL - 1)) * V + (V == 8 ? b5 * 4 + b4 * 2 + b3 : b5 * 2 + b4);
@@ -307,12 +308,12 @@ __device__ __forceinline__ int lane_token() {
 
 // Sums of NS sets of per-token values over the whole workgroup: tot[set][token], the same
 // bits for every thread. `red`: [waves][NS][TL * V].
-template <int TL, int V, int NS, int NT>
+template <int V, int NS, int NT>
 __device__ __forceinline__ void strip_total(const float (&f)[NS][V], float* red, float* tot) {
     constexpr int TT = TL * V, W = NT / 64;
-    const int t = lane_token<TL, V>();
+    const int t = lane_token<V>();
 #pragma unroll
-    for (int s = 0; s < NS; ++s) red[((threadIdx.x >> 6) * NS + s) * TT + t] = strip_sum<TL, V>(f[s]);
+    for (int s = 0; s < NS; ++s) red[((threadIdx.x >> 6) * NS + s) * TT + t] = strip_sum<V>(f[s]);
     __syncthreads();
     if (threadIdx.x < NS * TT) {
         float v = 0.0f;
@@ -357,7 +358,7 @@ __device__ __forceinline__ T* at_bytes(T* base, O off) {
 
 // NCH > 0: the strip is held in registers, NCH pieces a thread (all but the last within C).
 // NCH = 0 (more channels than that, or EDGE): it is read again for each use, from the caches.
-template <typename T, int NCH, int TL, int NT, bool EDGE>
+template <typename T, int NCH, int NT, bool EDGE>
 __global__ __launch_bounds__(NT) void layer_norm_strips_kernel(NormArgs a) {
     static_assert(!EDGE || NCH == 0, "pieces that end with the slab are not held");
     constexpr int V = Piece<T>::V, R = NT / TL, TT = TL * V, HOLD = NCH > 0 ? NCH : 1;
@@ -400,7 +401,7 @@ __global__ __launch_bounds__(NT) void layer_norm_strips_kernel(NormArgs a) {
 #pragma unroll
         for (int e = 0; e < V; ++e) f[0][e] += Piece<T>::get(p, e);
     }
-    strip_total<TL, V, 1, NT>(f, red, tot[0]);
+    strip_total<V, 1, NT>(f, red, tot[0]);
     float mean[V], rstd[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
@@ -418,7 +419,7 @@ __global__ __launch_bounds__(NT) void layer_norm_strips_kernel(NormArgs a) {
             }
         }
     }
-    strip_total<TL, V, 1, NT>(f, red, tot[1]);
+    strip_total<V, 1, NT>(f, red, tot[1]);
 #pragma unroll
     for (int e = 0; e < V; ++e) rstd[e] = 1.0f / sqrtf(tot[1][tl * V + e] * a.inv_c + a.eps);
 #pragma unroll NCH > 0 ? NCH : 1
@@ -446,11 +447,9 @@ __global__ __launch_bounds__(NT) void layer_norm_strips_kernel(NormArgs a) {
 }
 
 // Sum over the TL token lanes of a channel, in each of them.
-template <int TL>
 __device__ __forceinline__ float token_sum(float v) {
     v += dpp<kQuadXor1>(v);
     v += dpp<kQuadXor2>(v);
-    if constexpr (TL == 8) v += dpp<kHalfMirror>(v);
     return v;
 }
 
@@ -459,7 +458,7 @@ __device__ __forceinline__ float token_sum(float v) {
 // the arithmetic of the one before, with no registers of their own. Loads return in order,
 // so nothing else is loaded in between: gamma stays in registers, and a strip's statistics
 // are fetched ahead of its pieces.
-template <typename T, int NCH, int TL, int NT, bool SHIFT, bool EDGE>
+template <typename T, int NCH, int NT, bool SHIFT, bool EDGE>
 __global__ __launch_bounds__(NT) void layer_norm_strips_grad_kernel(NormArgs a) {
     static_assert(!EDGE || NCH == 0, "pieces that end with the slab are not held");
     constexpr int V = Piece<T>::V, R = NT / TL, TT = TL * V, HOLD = NCH > 0 ? NCH : 1;
@@ -548,15 +547,15 @@ __global__ __launch_bounds__(NT) void layer_norm_strips_grad_kernel(NormArgs a) 
                 __builtin_amdgcn_sched_barrier(0);
             } else {
                 // this thread alone writes the channel's sums of this workgroup
-                sg = token_sum<TL>(sg);
-                sb = token_sum<TL>(sb);
+                sg = token_sum(sg);
+                sb = token_sum(sb);
                 if (tl == 0 && c < a.C) {
                     out[c] = strip == strip0 ? sg : out[c] + sg;
                     out[a.C + c] = strip == strip0 ? sb : out[a.C + c] + sb;
                 }
             }
         }
-        strip_total<TL, V, 2, NT>(f, red, tot[0]);
+        strip_total<V, 2, NT>(f, red, tot[0]);
         // dx = rstd (d gamma - c1 - xhat c2) = d gamma rstd + (x - mean) t2 + t1
         float t1[V], t2[V];
 #pragma unroll
@@ -599,7 +598,7 @@ __global__ __launch_bounds__(NT) void layer_norm_strips_grad_kernel(NormArgs a) 
 #pragma unroll
         for (int i = 0; i < HOLD; ++i) {
             const int c = i * R + cr;
-            const float sg = token_sum<TL>(dg[i]), sb = token_sum<TL>(db[i]);
+            const float sg = token_sum(dg[i]), sb = token_sum(db[i]);
             if (tl == 0 && c < a.C) {
                 out[c] = sg;
                 out[a.C + c] = sb;
@@ -647,8 +646,8 @@ struct Derived {
     int64_t S = 0, M = 0, C = 0, sb = 0, ss = 0, sc = 0, x_span = 0;
     bool first = false, edge = false;   // channels-first; its slabs shorter than a strip
     int esize = 0, V = 0;
-    int tpr = 0, tl = 0, nt = 0, nch = 0;        // forward
-    int g_tpr = 0, g_tl = 0, g_nt = 0, g_nch = 0, parts = 0;   // backward
+    int tpr = 0, nt = 0, nch = 0;   // threads a row or strip, pieces a thread
+    int parts = 0;                  // backward: workgroups, and rows of the workspace
 };
 
 int64_t mul_cap(int64_t a, int64_t b) {
@@ -712,28 +711,23 @@ int check(const layer_norm_desc* d, Derived* out) {
     const int V = r.V, C = (int)r.C;
     if (!r.first) {
         // A wave a row while the row fits 4 pieces a lane (no barriers); else a workgroup.
-        const auto pick = [&](int& tpr, int& nch) {
-            tpr = C <= 64 * V * 4 ? 64 : C <= 256 * V * 4 ? 256 : 1024;
-            const int need = (C + tpr * V - 1) / (tpr * V);
-            nch = tpr == 1024 ? at_least(need, {2, 4, 8}) : at_least(need, {1, 2, 3, 4});
-        };
-        pick(r.tpr, r.nch);
-        pick(r.g_tpr, r.g_nch);
-        const int rpb = r.g_tpr < 512 ? 512 / r.g_tpr : 1;
+        r.tpr = C <= 64 * V * 4 ? 64 : C <= 256 * V * 4 ? 256 : 1024;
+        const int need = (C + r.tpr * V - 1) / (r.tpr * V);
+        r.nch = r.tpr == 1024 ? at_least(need, {2, 4, 8}) : at_least(need, {1, 2, 3, 4});
+        const int rpb = r.tpr < 512 ? 512 / r.tpr : 1;
         const int64_t want = (r.M + rpb - 1) / rpb;
         r.parts = (int)(want < 512 ? want : 512);
     } else {
         // as many threads as leave each 6 pieces or fewer
-        r.tl = r.g_tl = 4;
-        r.nt = r.g_nt = C <= 64 * 6 ? 256 : C <= 128 * 6 ? 512 : 1024;
+        r.nt = C <= 64 * 6 ? 256 : C <= 128 * 6 ? 512 : 1024;
         const int need = (C + r.nt / 4 - 1) / (r.nt / 4);
-        r.nch = r.g_nch = at_least(need, {1, 2, 3, 4, 5, 6});
+        r.nch = at_least(need, {1, 2, 3, 4, 5, 6});
         // held strips: slabs of a strip or more, offsets within a slab in 32 bits of bytes
-        r.edge = r.S < r.tl * V;
+        r.edge = r.S < TL * V;
         const int64_t reach = mul_cap(r.C, r.sc > r.S ? r.sc : r.S);
-        if (r.edge || reach < 0 || reach * r.esize > 2 * kMaxIndex) r.nch = r.g_nch = 0;
-        if (r.nch == 0) r.nt = r.g_nt = 1024;
-        const int64_t strips = mul_cap(d->batch, (r.S + r.g_tl * V - 1) / (r.g_tl * V)), turn = 256 * (1024 / r.g_nt);
+        if (r.edge || reach < 0 || reach * r.esize > 2 * kMaxIndex) r.nch = 0;
+        if (r.nch == 0) r.nt = 1024;
+        const int64_t strips = mul_cap(d->batch, (r.S + TL * V - 1) / (TL * V)), turn = 256 * (1024 / r.nt);
         r.parts = (int)(strips < turn ? strips : turn);
     }
     if (out) *out = r;
@@ -770,7 +764,7 @@ int on_device(const layer_norm_plan* h) {
     return dev == h->device ? FUSED_PROJ_OK : FUSED_PROJ_EINVAL;
 }
 
-NormArgs base_args(const layer_norm_plan* h, const void* x, const void* gamma, int tl) {
+NormArgs base_args(const layer_norm_plan* h, const void* x, const void* gamma) {
     const Derived& r = h->r;
     NormArgs a;
     std::memset(&a, 0, sizeof(a));
@@ -785,7 +779,7 @@ NormArgs base_args(const layer_norm_plan* h, const void* x, const void* gamma, i
     a.inv_c = (float)(1.0 / (double)r.C);
     a.eps = (float)h->d.eps;
     if (r.first) {
-        a.strips = (int32_t)((r.S + tl * r.V - 1) / (tl * r.V));
+        a.strips = (int32_t)((r.S + TL * r.V - 1) / (TL * r.V));
         a.all_strips = (int32_t)(h->d.batch * a.strips);
         a.div_s = fp::make_fastdiv_u31((uint32_t)a.strips);
     } else {
@@ -801,7 +795,7 @@ void launch(void (*kernel)(NormArgs), int64_t grid, int block, const NormArgs& a
 
 template <typename T, bool TAIL>
 void launch_rows(const Derived& r, const NormArgs& a, bool grad, hipStream_t st) {
-    const int tpr = grad ? r.g_tpr : r.tpr, nch = grad ? r.g_nch : r.nch;
+    const int tpr = r.tpr, nch = r.nch;
     const int block = tpr < (grad ? 512 : 256) ? (grad ? 512 : 256) : tpr, rpb = block / tpr;
     const int64_t want = (r.M + rpb - 1) / rpb, grid = grad ? r.parts : want < kMostBlocks ? want : kMostBlocks;
 #define LN_CASE(N, TPR)                                                                         \
@@ -818,15 +812,15 @@ void launch_rows(const Derived& r, const NormArgs& a, bool grad, hipStream_t st)
 template <typename T>
 void launch_strips(const Derived& r, const NormArgs& a, bool grad, hipStream_t st) {
     const int64_t grid = grad ? r.parts : a.all_strips;
-    const bool shift = r.S % (4 * Piece<T>::V) != 0;
+    const bool shift = r.S % (TL * Piece<T>::V) != 0;
     if (r.edge)
-        return launch(grad ? layer_norm_strips_grad_kernel<T, 0, 4, 1024, false, true> : layer_norm_strips_kernel<T, 0, 4, 1024, true>,
+        return launch(grad ? layer_norm_strips_grad_kernel<T, 0, 1024, false, true> : layer_norm_strips_kernel<T, 0, 1024, true>,
                       grid, 1024, a, st);
 #define LN_CASE(N, NT)                                                                                   \
     if (r.nt == NT && r.nch == N)                                                                        \
-        return launch(!grad   ? layer_norm_strips_kernel<T, N, 4, NT, false>                             \
-                      : shift ? layer_norm_strips_grad_kernel<T, N, 4, NT, true, false>                  \
-                              : layer_norm_strips_grad_kernel<T, N, 4, NT, false, false>,                \
+        return launch(!grad   ? layer_norm_strips_kernel<T, N, NT, false>                             \
+                      : shift ? layer_norm_strips_grad_kernel<T, N, NT, true, false>                  \
+                              : layer_norm_strips_grad_kernel<T, N, NT, false, false>,                \
                       grid, NT, a, st);
     LN_CASE(1, 256) LN_CASE(2, 256) LN_CASE(3, 256) LN_CASE(4, 256) LN_CASE(5, 256) LN_CASE(6, 256)
     LN_CASE(4, 512) LN_CASE(5, 512) LN_CASE(6, 512)
@@ -887,7 +881,7 @@ int layer_norm_run(layer_norm_t h, const void* x, const void* gamma, const void*
     if (overlap(ry, rs)) return FUSED_PROJ_EALIAS;
     const int rc = on_device(h);
     if (rc) return rc;
-    NormArgs a = base_args(h, x, gamma, r.tl);
+    NormArgs a = base_args(h, x, gamma);
     a.beta = bias ? beta : nullptr;
     a.y = y;
     a.mean = static_cast<float*>(stats);
@@ -937,7 +931,7 @@ int layer_norm_backward(layer_norm_t h, const void* x, const void* gamma, const 
     if (rc) return rc;
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (r.M > 0) {
-        NormArgs a = base_args(h, x, gamma, r.g_tl);
+        NormArgs a = base_args(h, x, gamma);
         a.dy = dy;
         a.y = dx;
         a.mean = const_cast<float*>(static_cast<const float*>(stats));
