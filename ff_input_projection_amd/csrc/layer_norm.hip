@@ -640,6 +640,9 @@ __global__ __launch_bounds__(1024) void layer_norm_columns_kernel(const float* p
 
 // ------------------------------------------------------------------ plans
 constexpr int64_t kMaxIndex = (int64_t(1) << 31) - 1;
+// Loops over tokens and strips step by up to 2^22 past the last (kMostBlocks workgroups of 4
+// rows) in 32 bits, and dgamma and dbeta are 2 C columns in 32 bits.
+constexpr int64_t kMostTokens = (int64_t(1) << 31) - (int64_t(1) << 23), kMostChannels = int64_t(1) << 29;
 constexpr int kMostBlocks = 1 << 20;   // along a grid's dimension, of up to 1024 threads: fewer than 2^32
 
 struct Derived {
@@ -686,7 +689,7 @@ int check(const layer_norm_desc* d, Derived* out) {
         if (r.S < 0) return FUSED_PROJ_EUNSUPPORTED;
     }
     r.M = mul_cap(d->batch, r.S);
-    if (r.M < 0 || r.M > kMaxIndex || r.S > kMaxIndex || r.C > kMaxIndex || mul_cap(r.M, r.C) < 0)
+    if (r.M < 0 || r.M > kMostTokens || r.S > kMostTokens || r.C > kMostChannels || mul_cap(r.M, r.C) < 0)
         return FUSED_PROJ_EUNSUPPORTED;
     r.sb = d->x_stride_batch;
     r.sc = d->x_stride_channel;

@@ -56,8 +56,8 @@ typedef struct layer_norm_plan *layer_norm_t;
 /* Host-only check. FUSED_PROJ_OK, FUSED_PROJ_EINVAL (malformed: sizes, enums, strides or
  * eps below 0) or FUSED_PROJ_EUNSUPPORTED: channels-first spatial strides that do not
  * flatten into one unit-stride token index, a tokens-last x_stride_channel other than 1
- * (either only where that stride is ever used), tokens-last C above 32768, or b*S, C or
- * b*S*C beyond 2^31 - 1, 2^31 - 1 or 2^60. Any C and S, odd ones too. */
+ * (either only where that stride is ever used), tokens-last C above 32768, or b*S, S, C or
+ * b*S*C beyond 2^31 - 2^23, the same, 2^29 or 2^60. Any C and S, odd ones too. */
 int layer_norm_validate(const layer_norm_desc *desc);
 
 /* Validates and picks the kernels; touches no GPU memory. Errors: as validate,
@@ -71,7 +71,7 @@ int layer_norm_create(const layer_norm_desc *desc, layer_norm_t *out);
  *   y      device, dense in x's logical shape ([b, C, S] or [b, S, C])
  *   stats  device fp32 [2, b*S]: the means, then the rstds; NULL when not wanted
  * Errors: FUSED_PROJ_EINVAL (NULL pointer, another device current), FUSED_PROJ_EALIGN (a
- * pointer not 16-byte aligned), FUSED_PROJ_EALIAS (y or stats overlapping each other or an
+ * pointer not aligned to its element), FUSED_PROJ_EALIAS (y or stats overlapping each other or an
  * input), FUSED_PROJ_EHIP. */
 int layer_norm_run(layer_norm_t plan, const void *x, const void *gamma, const void *beta, void *y, void *stats,
                    void *stream);
@@ -87,7 +87,7 @@ int layer_norm_backward_workspace_size(layer_norm_t plan, size_t *bytes);
  *   workspace device, layer_norm_backward_workspace_size bytes; contents do not matter.
  *             Calls that share a workspace must not overlap in time.
  * With no tokens dgamma and dbeta are set to zero. Errors as layer_norm_run; a short
- * workspace is FUSED_PROJ_EINVAL. */
+ * workspace is FUSED_PROJ_EINVAL, one not 16-byte aligned FUSED_PROJ_EALIGN. */
 int layer_norm_backward(layer_norm_t plan, const void *x, const void *gamma, const void *stats, const void *dy,
                         void *dx, void *dgamma, void *dbeta, void *workspace, size_t workspace_bytes, void *stream);
 

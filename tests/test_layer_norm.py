@@ -87,3 +87,15 @@ def test_python_refuses_what_is_no_activation():
         make_layer_norm_desc((2, 8, 4), (32, 4, 1), "tokens_last", torch.float16)
     with pytest.raises(fpa.FusedProjError):
         LayerNorm((2, 8, 5), (80, 10, 2), "tokens_last", torch.float32)
+
+
+@pytest.mark.parametrize("shape,strides,layout,code", [
+    ((1, (1 << 31) - (1 << 23), 1), (0, 0, 1), "tokens_last", fpa.OK),
+    ((1, (1 << 31) - (1 << 23) + 1, 1), (0, 0, 1), "tokens_last", fpa.EUNSUPPORTED),
+    (((1 << 31) - 1, 1, 1), (0, 0, 1), "channels_first", fpa.EUNSUPPORTED),
+    ((0, 1, (1 << 31) - 1), (0, 0, 1), "channels_first", fpa.EUNSUPPORTED),
+    ((1, 1 << 29, 1), (0, 0, 1), "channels_first", fpa.OK),
+    ((1, (1 << 29) + 1, 1), (0, 0, 1), "channels_first", fpa.EUNSUPPORTED),
+])
+def test_sizes_that_32_bit_loops_would_pass_are_refused(shape, strides, layout, code):
+    assert validate_layer_norm(_desc(shape, strides, layout)) == code
