@@ -192,7 +192,7 @@ def _planned_calls():
 
 def _planned_call(function: str, handle, slots):
     return _planned_calls().plan(ctypes.cast(getattr(load_library(), function), ctypes.c_void_p).value, handle.value,
-                                 slots)
+                                 torch.cuda.current_device(), slots)
 
 
 def _planned_call_function():

@@ -3,7 +3,7 @@
 // stream, collecting addresses) without the interpreter's share, about 1 us instead of 8. A
 // decoding step makes a few such calls for kernels of a few microseconds.
 //
-// plan(function address, handle, slots) makes the plan. A slot is an argument of the C
+// plan(function address, handle, device index, slots) makes the plan. A slot is an argument of the C
 // function, in its order; the handle comes first and the stream last:
 //   ("in" | "maybe", shape, strides or None, dtype)   a tensor (or None) that the caller gives
 //   ("out", shape, dtype)                             an output, allocated here
@@ -14,7 +14,7 @@
 // call(plan, ...) takes the tensors of the "in", "maybe" and "storage" slots in order, then the
 // workspace or None. It returns the tuple of outputs, an int status other than 0 of the C
 // function, or None if an argument is not what the plan says (the caller then finds out what
-// is wrong and says so). All tensors have to be on the first one's device.
+// is wrong and says so). All tensors have to be on the plan's device.
 #include <ATen/ATen.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -38,6 +38,7 @@ struct Slot {
 constexpr int kMostArgs = 12, kMostStorage = 8;
 struct Plan {
     uintptr_t fn, handle;
+    at::Device device;
     std::vector<Slot> slots;
     Py_ssize_t given = 0;   // arguments of call() behind the plan
     int outs = 0, args = 0;
@@ -111,9 +112,10 @@ bool add_slot(Plan* p, PyObject* t) {
 
 PyObject* plan(PyObject*, PyObject* args) {
     unsigned long long fn = 0, handle = 0;
+    int device = 0;
     PyObject* slots = nullptr;
-    if (!PyArg_ParseTuple(args, "KKO!:plan", &fn, &handle, &PyTuple_Type, &slots)) return nullptr;
-    Plan* p = new Plan{(uintptr_t)fn, (uintptr_t)handle, {}, 0, 0, 2};
+    if (!PyArg_ParseTuple(args, "KKiO!:plan", &fn, &handle, &device, &PyTuple_Type, &slots)) return nullptr;
+    Plan* p = new Plan{(uintptr_t)fn, (uintptr_t)handle, at::Device(at::kCUDA, (at::DeviceIndex)device), {}, 0, 0, 2};
     try {
         for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(slots); ++i)
             if (!add_slot(p, PyTuple_GET_ITEM(slots, i))) {
@@ -135,23 +137,12 @@ PyObject* plan(PyObject*, PyObject* args) {
     return PyCapsule_New(p, "planned call", free_plan);
 }
 
-struct Device {
-    at::Device at{at::kCPU};
-    bool set = false;
-};
-
-bool fits(PyObject* o, const Spec& s, Device* dev, uintptr_t* address) {
+bool fits(PyObject* o, const Spec& s, at::Device device, uintptr_t* address) {
     if (!THPVariable_Check(o)) return false;
     const at::Tensor& t = THPVariable_Unpack(o);
     if (t.scalar_type() != s.dtype || t.layout() != at::kStrided || t.sizes() != s.shape) return false;
     if (s.dense ? !t.is_contiguous() : t.strides() != s.strides) return false;
-    if (!dev->set) {
-        if (!t.is_cuda()) return false;
-        dev->at = t.device();
-        dev->set = true;
-    } else if (t.device() != dev->at) {
-        return false;
-    }
+    if (t.device() != device) return false;
     *address = reinterpret_cast<uintptr_t>(t.data_ptr());
     return true;
 }
@@ -183,34 +174,32 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
     try {
         uintptr_t a[kMostArgs], storage[kMostStorage];
         at::Tensor outs[4], workspace;
-        Device dev;
         Py_ssize_t next = 1;
-        // the given tensors first: they say which device the rest is on
+        // the given tensors first: nothing is allocated for a call that is not the plan's
         int at = 1;
         for (const Slot& s : p->slots) {
             if (s.kind == kIn || s.kind == kMaybe) {
                 PyObject* o = args[next++];
                 if (s.kind == kMaybe && o == Py_None)
                     a[at] = 0;
-                else if (!fits(o, s.specs[0], &dev, &a[at]))
+                else if (!fits(o, s.specs[0], p->device, &a[at]))
                     Py_RETURN_NONE;
             } else if (s.kind == kStorage) {
                 PyObject* o = args[next++];
                 if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != (Py_ssize_t)s.specs.size()) Py_RETURN_NONE;
                 for (size_t i = 0; i < s.specs.size(); ++i)
-                    if (!fits(PyTuple_GET_ITEM(o, i), s.specs[i], &dev, &storage[i])) Py_RETURN_NONE;
+                    if (!fits(PyTuple_GET_ITEM(o, i), s.specs[i], p->device, &storage[i])) Py_RETURN_NONE;
                 a[at] = reinterpret_cast<uintptr_t>(storage);
             } else if (s.kind == kWorkspace) {
                 ++at;
             }
             ++at;
         }
-        if (!dev.set) Py_RETURN_NONE;
         int n_out = 0;
         at = 1;
         for (const Slot& s : p->slots) {
             if (s.kind == kOut) {
-                outs[n_out] = at::empty(s.specs[0].shape, at::TensorOptions().dtype(s.specs[0].dtype).device(dev.at));
+                outs[n_out] = at::empty(s.specs[0].shape, at::TensorOptions().dtype(s.specs[0].dtype).device(p->device));
                 a[at] = reinterpret_cast<uintptr_t>(outs[n_out++].data_ptr());
             } else if (s.kind == kWorkspace) {
                 PyObject* o = args[n - 1];
@@ -221,11 +210,11 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
                     continue;
                 }
                 if (o == Py_None) {
-                    workspace = at::empty({bytes}, at::TensorOptions().dtype(at::kByte).device(dev.at));
+                    workspace = at::empty({bytes}, at::TensorOptions().dtype(at::kByte).device(p->device));
                 } else {
                     if (!THPVariable_Check(o)) Py_RETURN_NONE;
                     workspace = THPVariable_Unpack(o);
-                    if (workspace.device() != dev.at || !workspace.is_contiguous()) Py_RETURN_NONE;
+                    if (workspace.device() != p->device || !workspace.is_contiguous()) Py_RETURN_NONE;
                     bytes = (int64_t)workspace.nbytes();
                 }
                 a[at++] = reinterpret_cast<uintptr_t>(workspace.data_ptr());
@@ -233,7 +222,7 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
             }
             ++at;
         }
-        PyObject* index = PyLong_FromLong(dev.at.index());
+        PyObject* index = PyLong_FromLong(p->device.index());
         if (!index) return nullptr;
         PyObject* stream = PyObject_CallOneArg(g_raw_stream, index);
         Py_DECREF(index);
@@ -269,7 +258,7 @@ PyObject* set_raw_stream(PyObject*, PyObject* f) {
 }
 
 PyMethodDef kMethods[] = {
-    {"plan", plan, METH_VARARGS, "plan(function address, handle, slots): a planned call."},
+    {"plan", plan, METH_VARARGS, "plan(function address, handle, device index, slots): a planned call."},
     {"call", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call)), METH_FASTCALL,
      "call(plan, tensors..., workspace or None): outputs, a status, or None."},
     {"set_raw_stream", set_raw_stream, METH_O, "The function from a device's index to its current stream's address."},

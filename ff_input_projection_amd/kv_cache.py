@@ -38,7 +38,8 @@ class KVCache:
     ``read`` returns the step's rows as the values they stand for; ``attend`` returns
     [batch, tokens, H*hd], the step's queries q [batch*H, tokens, hd] over all that the cache
     holds up to each. Launches go to torch's current stream (or ``stream``) and are
-    asynchronous.
+    asynchronous. A plan belongs to the device that was current when it was made: its tensors
+    are on that device, and it is the current one in every call.
     """
 
     def __init__(self, batch: int, tokens: int, n_heads: int, head_dim: int, **kw):
@@ -50,7 +51,7 @@ class KVCache:
         rc = self._lib.kv_cache_create(ctypes.byref(d), ctypes.byref(h))
         if rc != OK:
             raise FusedProjError(rc, "kv_cache_create")
-        self._h = h
+        self._h, self._device = h, torch.cuda.current_device()
         self._table_shape, self._kv_shape = (batch, d.max_pages), (batch * self.KVH, tokens, head_dim)
         self._q_shape, self._o_shape = (batch * n_heads, tokens, head_dim), (batch, tokens, n_heads * head_dim)
         slots = (d.n_pages, self.KVH, d.page_size)
@@ -99,6 +100,8 @@ class KVCache:
     def _cache(self, storage, table, lengths, counts, device):
         if device.type != "cuda":
             raise TypeError("the cache and its inputs are GPU tensors")
+        if device.index != self._device:
+            raise ValueError(f"the plan is for cuda:{self._device}, not for {device}")
         kc, kp, vc, vp = storage
         self._check("k_codes", kc, self._codes_shape, torch.uint8, device)
         self._check("k_params", kp, self._params_shape, torch.bfloat16, device)

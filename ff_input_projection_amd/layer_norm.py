@@ -42,6 +42,8 @@ class LayerNorm:
     [2, b*S] with every token's mean and 1 / standard deviation (what ``backward`` takes).
     ``backward`` returns ``(dx, dgamma, dbeta)``, dbeta None without a bias. Outputs may be
     passed in; the launches go to torch's current stream (or ``stream``) and are asynchronous.
+    A plan belongs to the device that was current when it was made: its tensors are on that
+    device, and it is the current one in every call.
     """
 
     def __init__(self, x_shape, x_strides, layout: str, dtype: torch.dtype, *, eps: float = 1e-5, has_bias: bool = True):
@@ -56,7 +58,7 @@ class LayerNorm:
         rc = self._lib.layer_norm_create(ctypes.byref(self.desc), ctypes.byref(h))
         if rc != OK:
             raise FusedProjError(rc, "layer_norm_create")
-        self._h = h
+        self._h, self._device = h, torch.cuda.current_device()
         n = ctypes.c_size_t()
         rc = self._lib.layer_norm_backward_workspace_size(self._h, ctypes.byref(n))
         if rc != OK:
@@ -90,6 +92,8 @@ class LayerNorm:
                              f"{self.x_strides}")
         if x.dtype != self.dtype or not x.is_cuda:
             raise TypeError(f"x must be a {self.dtype} GPU tensor")
+        if x.device.index != self._device:
+            raise ValueError(f"the plan is for cuda:{self._device}, not for {x.device}")
 
     def _check(self, name, t, shape, device, dtype=None):
         if t is None or t.shape != shape or not t.is_contiguous() or t.dtype != (dtype or self.dtype) or t.device != device:

@@ -503,3 +503,19 @@ def test_a_block_in_serving(bits):
             flat, ftol = want.reshape(tokens, -1), tol.reshape(tokens, -1)
             bound = ftol @ np.abs(w) + 2.0 ** -8 * np.abs(flat @ w) + (256 + 8) * ref.U * (np.abs(flat) @ np.abs(w)) * 2
             within(out[i].double().cpu().numpy(), flat @ w, bound + 2.0 ** -8 * (ftol @ np.abs(w)))
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """A plan made where another device was current takes no tensors of this one."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    plan = KVCache(1, 1, 2, 64, n_pages=2, max_pages=1)
+    monkeypatch.undo()
+    storage = plan.alloc_storage(DEV)
+    k, v, q = (torch.zeros((2, 1, 64), dtype=torch.bfloat16, device=DEV) for _ in range(3))
+    meta = (torch.zeros((1, 1), **I32), torch.ones((1,), **I32))
+    with pytest.raises(ValueError):
+        plan.write(storage, k, v, *meta)
+    with pytest.raises(ValueError):
+        plan.read(storage, *meta)
+    with pytest.raises(ValueError):
+        plan.attend(storage, q, *meta)

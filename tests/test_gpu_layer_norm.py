@@ -377,3 +377,17 @@ def test_more_tokens_than_one_dimension_of_a_grid(layout):
     for got, terms in ((dgamma, d * xhat), (dbeta, d)):
         # up to 5000 additions a thread: their roundings add up to 5000 u of the sum of magnitudes at most
         assert ((got.double() - terms.sum(other)).abs() <= 6000 * U * (terms.abs() + d.abs()).sum(other)).all()
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """A plan made where another device was current takes no tensors of this one, in either path."""
+    x, gamma, beta, dy = make("tokens_last", B, 2, 64, (5,), 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    ln = LayerNorm.for_tensor(x, "tokens_last")
+    monkeypatch.undo()
+    with pytest.raises(ValueError):
+        ln(x, gamma, beta)
+    with pytest.raises(ValueError):
+        ln(x, gamma, beta, out=(torch.empty_like(x), None))
+    with pytest.raises(ValueError):
+        ln.backward(x, gamma, torch.zeros((2, 10), device=DEV), dy)
