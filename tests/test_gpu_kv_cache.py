@@ -519,3 +519,31 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
         plan.read(storage, *meta)
     with pytest.raises(ValueError):
         plan.attend(storage, q, *meta)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("tokens", [3, 40])
+@pytest.mark.parametrize("where", ["padding", "head"])
+def test_attend_queries_of_different_sizes_side_by_side(where, tokens, bits):
+    """Rows of up to 2^89 beside ordinary and small ones: in the padding's place they do not show at all, as another head's
+    they leave the others' accuracy (whose bound knows nothing of them)."""
+    c = Case(bits, 2, tokens, 4, 2, 64, 16, 8, [120, 121], [tokens - 1, tokens - 2], seed=11)
+    storage = c.dirty_storage()
+    c.fill(storage)
+    q = c.queries()
+    qv = q.view(2, 4, tokens, 64)
+    qv[:, 3] *= 2.0 ** -6
+    clean = c.attend(storage, q)
+    if where == "padding":
+        qv[0, :, tokens - 1:] = 1.5 * 2.0 ** 89
+        qv[1, :, tokens - 2:] = 1.5 * 2.0 ** 89
+        o = c.attend(storage, q)
+        within(o, *c.expected(q))
+        assert np.array_equal(o, clean)
+    else:
+        qv[:, 2] *= 2.0 ** 80
+        o = c.attend(storage, q)
+        want, tol = c.expected(q)
+        rest = [0, 1, 3]
+        within(o[:, :, rest], want[:, :, rest], tol[:, :, rest])
+        assert np.isfinite(o).all()
