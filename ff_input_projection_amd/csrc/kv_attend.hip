@@ -26,8 +26,8 @@
 // operand shares. V's operand needs 8 positions of one element in a lane: a lane reads the
 // same few bytes of 8 positions and pairs them up with byte permutes.
 //
-// Measured, 4 bits, 32 heads on 8 x 128: 63 sequences of 8191 positions, one token each, 106 us
-// (5.3 TB/s, a large copy's rate; 42% of the vector pipes' time); of 2500 to 8191 positions 83
+// Measured, 4 bits, 32 heads on 8 x 128: 63 sequences of 8191 positions, one token each, 105 us
+// (5.3 TB/s, a large copy's rate; 42% of the vector pipes' time); of 2500 to 8191 positions 79
 // us; 2 x 1024 tokens over 4096 positions 185 us (650 TFLOP/s; a large bf16 product reaches
 // 1209).
 #include <cmath>
@@ -865,9 +865,14 @@ bool plan_attend(const kv_cache_desc& d, int64_t kvh, AttendPlan* out) {
     // Parts of a sequence, equal ones whatever its length (which the device alone knows):
     // enough workgroups to fill the card, with parts long enough to be worth their queries and
     // their join. Parts of one size for all sequences measured slower (104 us instead of 84
-    // for 64 sequences of 2500 to 8191 positions).
-    const int64_t positions = d.max_pages * d.page_size, want = p.chunk ? 512 : 1024, least = p.chunk ? 512 : 256;
-    int64_t splits = (want + heads * p.row_blocks - 1) / (heads * p.row_blocks);
+    // for 64 sequences of 2500 to 8191 positions). Few rows: half as many workgroups again
+    // where parts are longer than 2048 positions, so that long sequences end together with
+    // short ones (63 sequences up to 8191: 83 -> 79 us); where parts are shorter, their
+    // number costs more than it gives (24 of up to 3333: 22.5 -> 23.2 us).
+    const int64_t positions = d.max_pages * d.page_size, least = p.chunk ? 512 : 256;
+    const auto parts = [&](int64_t want) { return (want + heads * p.row_blocks - 1) / (heads * p.row_blocks); };
+    const int64_t want = p.chunk ? 512 : positions > 2048 * parts(1024) ? 1536 : 1024;
+    int64_t splits = parts(want);
     if (p.chunk && 4 * heads * p.row_blocks > 3 * want) splits = 1;
     if (splits > (positions + least - 1) / least) splits = (positions + least - 1) / least;
     p.splits = (int32_t)(splits < 1 ? 1 : splits > 64 ? 64 : splits);
