@@ -547,3 +547,47 @@ def test_attend_queries_of_different_sizes_side_by_side(where, tokens, bits):
         rest = [0, 1, 3]
         within(o[:, :, rest], want[:, :, rest], tol[:, :, rest])
         assert np.isfinite(o).all()
+
+
+def test_captured_calls_that_allocate():
+    """A step captured without outputs or workspaces of its own, on another stream than the default one: each replay gives
+    the eager step's bits, for new contents of the same tensors too."""
+    b, H, KVH, hd, page, pages = 3, 8, 2, 64, 16, 30
+    g = torch.Generator(device=DEV).manual_seed(12)
+    rand = lambda *s: torch.randn(s, generator=g, device=DEV).to(torch.bfloat16)
+    plan = KVCache(b, 1, H, hd, n_kv_heads=KVH, page_size=page, n_pages=b * pages, max_pages=pages)
+    assert plan.workspace_bytes() > 0
+    storage = plan.alloc_storage(DEV)
+    table = torch.randperm(b * pages, generator=g, device=DEV).view(b, pages).to(torch.int32)
+    x, gamma, beta = rand(b, 1, H * hd), rand(H * hd), rand(H * hd)
+    norm = LayerNorm.for_tensor(x, "tokens_last")
+    lengths = torch.tensor([1, 400, 479], **I32)
+    k, v = rand(b * KVH, 1, hd), rand(b * KVH, 1, hd)
+
+    def step():
+        y, stats = norm(x, gamma, beta)
+        plan.write(storage, k, v, table, lengths)
+        o = plan.attend(storage, y.view(b * H, 1, hd), table, lengths)
+        return (y, stats, o, *plan.read(storage, table, lengths), *norm.backward(x, gamma, stats, o))
+
+    for n in (400, 470):     # something to look back at
+        plan.write(storage, rand(b * KVH, 1, hd), rand(b * KVH, 1, hd), table, torch.full((b,), n, **I32))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            outs = step()
+    torch.cuda.current_stream().wait_stream(side)
+    for i in range(3):
+        want = [t.clone() for t in step()]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, e in zip(outs, want):
+            assert torch.equal(a, e)
+        x.copy_(rand(b, 1, H * hd))
+        k.copy_(rand(b * KVH, 1, hd))
+        lengths.add_(1 if i == 0 else 0)
+        torch.cuda.synchronize()
