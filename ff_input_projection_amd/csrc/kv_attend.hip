@@ -12,6 +12,7 @@
 // The affine format stays outside the products. With a token's scale s and zero z,
 //   q . khat = s (q . c) + z sum(q)
 //   sum_j p_j vhat_j = sum_j b_j (c_j - C) + sum_j p_j (z_j + C s_j),    b_j = p_j s_j in bf16
+// The second sum is kept apart from the codes' powers of two: zero has no bound as s has one.
 // C is the middle code: codes are positive, so the rounding of b_j times c_j would be that of
 // a sum far larger than the result; times c_j - C it is the rounding of the values' own
 // spread (measured: output error 0.0023 of the output's norm instead of 0.0049, of which
@@ -41,8 +42,13 @@ using namespace fp::dev;
 using fp::CacheArgs;
 
 constexpr float kLowest = -3.0e38f;   // the running maximum before any position
-constexpr float kLift = 80.0f;        // probabilities are held times 2^80: with a scale of at most 2^24 and
-                                      // codes of 2^-133 their products neither overflow nor vanish
+// Probabilities are held times 2^-24: zero + C scale may be any bfloat16 number (a row of one value
+// is kept whatever its size), and the largest, under probabilities of up to 2^kSlack, still adds up
+// over 2^16 positions, while numbers down to 2^-117 keep the 8 bits that o has. v's scales (at most
+// 2^24) are taken times 2^103 instead: their products with probabilities and codes of 2^-133
+// neither overflow nor vanish.
+constexpr float kLift = -24.0f;
+constexpr uint32_t kScaleLift = 103;
 constexpr float kSlack = 8.0f;        // how far (log2) a logit may pass the running maximum before it moves
 
 template <int D, int BITS>
@@ -154,7 +160,7 @@ template <int D, int R>
 struct State {
     f32x4 o[R][D / 16];    // output tiles, in codes: see each_run
     f32x4 c[R];               // 2 C sum_j b_j, in codes: the same in all four
-    float m[R], l[R], z[R];   // running maximum (log2), and this lane's sums of p and of p (z + C s)
+    float m[R], l[R], z[R];   // running maximum (log2), and this lane's sums of p and of p (z + C s), times 2^-24
 };
 template <int D, int R>
 __device__ __forceinline__ void clear(State<D, R>& st) {
@@ -169,13 +175,17 @@ __device__ __forceinline__ void clear(State<D, R>& st) {
 }
 
 // The affine part of a lane's 8 positions (two halves of 4): k's scale times the logits'
-// factor, k's zero, v's scale, v's zero + C times its scale.
+// factor, k's zero, v's scale times 2^103, v's zero + C times its scale.
 struct Affine {
     float ks[2][4], kz[2][4], vs[2][4], vz[2][4];
 };
+// By the exponent, with the shift that unpacks it: a scale of 0 or a denormal one becomes another of
+// 2^-126 or less, here and in `middle`. A NaN becomes a number: its row's zero is NaN too.
+__device__ __forceinline__ float lifted_scale(uint32_t w) { return __uint_as_float((w << 16) + (kScaleLift << 23)); }
 template <int BITS>
 __device__ __forceinline__ float middle(uint32_t w) {
-    return fmaf(param_scale(w), 0.5f * (float)((1 << BITS) - 1), param_zero(w));
+    static_assert(kScaleLift == 103, "the factor that takes the lift back");
+    return fmaf(lifted_scale(w), 0x1p-103f * 0.5f * (float)((1 << BITS) - 1), param_zero(w));
 }
 
 // What hides positions from the wave's rows: the halves' existing positions, the tile's first
@@ -289,7 +299,7 @@ __device__ __forceinline__ void take_tile(State<D, R>& st, const Tile<D, BITS>& 
         for (int i = 0; i < 4; ++i) {
             af.ks[u][i] = param_scale(t.kp[u][i]) * c1;
             af.kz[u][i] = param_zero(t.kp[u][i]);
-            af.vs[u][i] = param_scale(t.vp[u][i]);
+            af.vs[u][i] = lifted_scale(t.vp[u][i]);
             af.vz[u][i] = middle<BITS>(t.vp[u][i]);
         }
     f32x4 s[R][2];
@@ -342,8 +352,8 @@ __device__ __forceinline__ void take_tile(State<D, R>& st, const Tile<D, BITS>& 
 }
 
 // Calls f(d, values) for each run of consecutive elements d .. d + N - 1 that the lane holds of
-// its row, the values still to be divided by the row's sum. The lift ends here: codes of 2^-133
-// under probabilities of 2^80 come back by 2^53 (the 4-bit codes masked 4 bits up by 2^49).
+// its row, still to be divided by the row's sum (both times 2^-24). The lift ends here: codes of
+// 2^-133 times scales of 2^103 come back by 2^30 (the 4-bit codes masked 4 bits up by 2^26).
 template <int D, int BITS, int R, typename F>
 __device__ __forceinline__ void each_run(const State<D, R>& st, int r, float z, F f) {
     using Sh = Shape<D, BITS>;
@@ -354,7 +364,7 @@ __device__ __forceinline__ void each_run(const State<D, R>& st, int r, float z, 
         for (int i = 0; i < 4; ++i) {
             float v[N];
 #pragma unroll
-            for (int k = 0; k < N; ++k) v[k] = fmaf(st.o[r][T0 + k][i], BITS == 4 && (k & 1) ? 0x1p49f : 0x1p53f, z);
+            for (int k = 0; k < N; ++k) v[k] = fmaf(st.o[r][T0 + k][i], BITS == 4 && (k & 1) ? 0x1p26f : 0x1p30f, z);
             f(T0 * 16 + (qd * 4 + i) * N, v);
         }
     };
@@ -522,8 +532,8 @@ __global__ __launch_bounds__(256, (kStepWaves<D, BITS, R>)) void kv_attend_kerne
 
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const float l = sum_over_quads(st.l[r]) * 0x1p-80f;
-        const float z = fmaf(st.c[r][0], -0x1p52f, sum_over_quads(st.z[r]) * 0x1p-80f);
+        const float l = sum_over_quads(st.l[r]);
+        const float z = fmaf(st.c[r][0], -0x1p29f, sum_over_quads(st.z[r]));
         // the workgroup's waves together, 16 rows at a time
         if (r > 0) __syncthreads();
         float* mine = both + (wave * 16 + n) * PAD;
@@ -645,7 +655,7 @@ __device__ __forceinline__ void share_raw(Shared<D, BITS, NW>& to, const Raw<D, 
     if (lane < 16) {
         to.affine[0][wave * 16 + lane] = param_scale(t.kp) * c1;
         to.affine[1][wave * 16 + lane] = param_zero(t.kp);
-        to.affine[2][wave * 16 + lane] = param_scale(t.vp);
+        to.affine[2][wave * 16 + lane] = lifted_scale(t.vp);
         to.affine[3][wave * 16 + lane] = middle<BITS>(t.vp);
     }
     if (lane == 0) to.known[wave] = t.known;
@@ -764,8 +774,8 @@ __global__ __launch_bounds__(NW * 64, 2) void kv_attend_chunk_kernel(CacheArgs a
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const float l = sum_over_quads(st.l[r]) * 0x1p-80f;
-        const float z = fmaf(st.c[r][0], -0x1p52f, sum_over_quads(st.z[r]) * 0x1p-80f);
+        const float l = sum_over_quads(st.l[r]);
+        const float z = fmaf(st.c[r][0], -0x1p29f, sum_over_quads(st.z[r]));
         if (!w.real[r]) continue;
         if (a.splits == 1) {
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;

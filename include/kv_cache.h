@@ -40,11 +40,12 @@
  *
  * and 0 for a padding token, or where no position is seen. Products of q and codes are
  * exact, sums, softmax and statistics fp32, the probabilities (times v's scale) rounded to
- * bfloat16 for the second product, o rounded once. A query row that holds a NaN, an infinity
- * or a value of 2^90 or more gives NaN where it sees any position; so does every row that
- * sees a row kept as NaN. Positions that a token does not see never reach its output,
- * whatever their slots hold. Softmax over tiles with a running maximum and sum: Milakov and
- * Gimelshein, "Online normalizer calculation for softmax", 2018.
+ * bfloat16 for the second product, o rounded once. Rows of v may hold numbers of any size;
+ * besides its roundings o is off by up to about 2^-90, where products with codes vanish. A
+ * query row that holds a NaN, an infinity or a value of 2^90 or more gives NaN where it sees
+ * any position; so does every row that sees a row kept as NaN. Positions that a token does
+ * not see never reach its output, whatever their slots hold. Softmax over tiles with a running
+ * maximum and sum: Milakov and Gimelshein, "Online normalizer calculation for softmax", 2018.
  *
  * Errors are the FUSED_PROJ_* codes; fused_proj_strerror() describes them. A plan only holds
  * sizes, so it may be used from several host threads and streams at once. Calls that write

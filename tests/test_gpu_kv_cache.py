@@ -591,3 +591,28 @@ def test_captured_calls_that_allocate():
         k.copy_(rand(b * KVH, 1, hd))
         lengths.add_(1 if i == 0 else 0)
         torch.cuda.synchronize()
+
+
+LARGE_V = [  # bits, batch, tokens, heads, kvh, hd, page, max_pages, lengths: both kernels, one part and joined ones
+    (4, 2, 1, 8, 2, 64, 16, 40, [640, 33]), (8, 1, 3, 2, 1, 256, 16, 100, [1600]), (4, 2, 1, 4, 2, 96, 16, 2, [30, 9]),
+    (4, 1, 40, 4, 2, 128, 64, 40, [2560]), (8, 2, 200, 4, 4, 32, 64, 64, [4096, 4000]), (4, 1, 70, 2, 1, 192, 16, 9, [140]),
+]
+
+
+@pytest.mark.parametrize("power", [-100, 30, 40, 60, 100, 127])
+@pytest.mark.parametrize("case", LARGE_V, ids=[f"{c[0]}bit_t{c[2]}_x{c[5]}" for c in LARGE_V])
+def test_attend_constant_values_of_any_size(case, power):
+    """Rows of one value are kept exactly (scale 0), whatever its size: alone in the first k/v head of the first sequence,
+    beside ordinary rows and with both signs elsewhere."""
+    c = Case(*case, None, seed=14)
+    shape = (c.batch, c.kvh, c.capacity, c.hd)
+    v = c.random(*shape)
+    size = torch.tensor(1.5 * 2.0 ** power).to(torch.bfloat16)
+    v[:, :, 0::2] = size
+    v[:, :, 0::6] = -size
+    v[0, 0] = size
+    storage = c.dirty_storage()
+    c.fill(storage, None, v)
+    q = c.queries()
+    want, tol = c.expected(q)
+    within(c.attend(storage, q), want, tol)
