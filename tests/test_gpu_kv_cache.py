@@ -616,3 +616,20 @@ def test_attend_constant_values_of_any_size(case, power):
     q = c.queries()
     want, tol = c.expected(q)
     within(c.attend(storage, q), want, tol)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("tokens", [3, 40])
+def test_attend_padding_beside_keys_of_large_scales(tokens, bits):
+    """What lies in the padding's place of q does not show: not at the largest sizes either, over keys of scales of 2^14 and more."""
+    c = Case(bits, 2, tokens, 4, 2, 64, 16, 8, [120, 121], [tokens - 1, tokens - 2], seed=15)
+    storage = c.dirty_storage()
+    c.fill(storage, c.random(2, 2, 128, 64) * 2.0 ** 20)
+    q = c.queries() * 2.0 ** -20
+    clean = c.attend(storage, q)
+    within(clean, *c.expected(q))
+    qv = q.view(2, 4, tokens, 64)
+    for junk in (1.5 * 2.0 ** 89, float("nan"), 3.3e38):
+        qv[0, :, tokens - 1:] = junk
+        qv[1, :, tokens - 2:] = junk
+        assert np.array_equal(c.attend(storage, q), clean)
