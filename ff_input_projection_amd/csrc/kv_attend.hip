@@ -6,8 +6,9 @@
 // cores take denormal inputs as they are. So a code becomes an operand by masking alone,
 // and its products with q are exact. With 4 bits, every other code is masked where it lies,
 // 4 bits up, and stands for 16 c 2^-133: those elements of q are divided by 16, those of the
-// output at the end. q is multiplied by the power of two that brings the wave's largest
-// value to 2^100, so that the products are ordinary numbers.
+// output at the end. q is multiplied by the power of two that brings the wave's largest value
+// to 2^126, so that the products are ordinary numbers (sums of 256 stay below 2^11) and the
+// factor that takes them back is small: it is multiplied by k's scales.
 //
 // The affine format stays outside the products. With a token's scale s and zero z,
 //   q . khat = s (q . c) + z sum(q)
@@ -395,7 +396,7 @@ struct Rows {
 };
 
 // The rows' places and their own positions, and their queries' bits; returns the largest
-// exponent field among the lane's rows whose values are all below 2^90 (others give NaN).
+// exponent field among the lane's rows whose values are all below q_limit (others give NaN).
 template <int D, int BITS, int R>
 __device__ __forceinline__ uint32_t find_rows(Rows<D, BITS, R>& w, u32x4 (&raw)[R][D / 32], bool (&bad)[R], const CacheArgs& a,
                                               const fp::Step& step, int seq, int kvh, int row0) {
@@ -420,7 +421,7 @@ __device__ __forceinline__ uint32_t find_rows(Rows<D, BITS, R>& w, u32x4 (&raw)[
         }
         mine = max(mine, (uint32_t)__shfl_xor((int)mine, 16));
         mine = max(mine, (uint32_t)__shfl_xor((int)mine, 32));
-        bad[r] = mine >= 127 + 90;
+        bad[r] = mine >= (uint32_t)a.q_limit;
         top = max(top, bad[r] ? 0u : mine);
     }
 #pragma unroll
@@ -453,9 +454,10 @@ __device__ __forceinline__ void lift_rows(Rows<D, BITS, R>& w, const u32x4 (&raw
         w.zq[r] = bad[r] ? NAN : sum * logit_scale;
     }
 }
-// q's lift that brings the exponent field `top` to 2^100, and the factor that takes the
-// products back.
-__device__ __forceinline__ int lift_of(uint32_t top) { return 100 - ((int)max(top, 1u) - 127); }
+// q's lift that brings the exponent field `top` to 2^126, and the factor that takes the products
+// back: 2^(7 + e) logit_scale for a largest value of 2^e, at most 2^103 by q_limit. With k's scale
+// (at most 2^24) that is a finite number for every row, whatever row of the workgroup is largest.
+__device__ __forceinline__ int lift_of(uint32_t top) { return 126 - ((int)max(top, 1u) - 127); }
 __device__ __forceinline__ float logits_factor(int lift, float logit_scale) { return ldexpf(logit_scale, 133 - lift); }
 
 // Which part of the work a workgroup takes. k/v heads run fastest: the workgroups of one

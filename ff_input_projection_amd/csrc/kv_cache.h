@@ -30,6 +30,7 @@ struct CacheArgs {
     int32_t row_blocks;        // attend: workgroups over a k/v head's query rows
     int32_t splits;            // attend: parts that a sequence's positions are cut into
     float logit_scale;         // sm_scale log2(e)
+    int32_t q_limit;           // the exponent field from which on a query's values are too large
     FastDivU31 div_t, div_kvh, div_page, div_group, div_blocks;
 };
 

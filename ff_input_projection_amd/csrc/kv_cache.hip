@@ -195,6 +195,12 @@ struct Derived {
     int lpr = 0;
 };
 
+// Logits are in units of log 2.
+float logits_factor(const kv_cache_desc& d) {
+    const double scale = d.sm_scale > 0.0 ? d.sm_scale : 1.0 / std::sqrt((double)d.head_dim);
+    return (float)(scale * 1.4426950408889634074);
+}
+
 int check(const kv_cache_desc* d, Derived* out) {
     if (!d) return FUSED_PROJ_EINVAL;
     if (d->dtype != FUSED_PROJ_BF16 && d->dtype != FUSED_PROJ_F32) return FUSED_PROJ_EINVAL;
@@ -202,7 +208,7 @@ int check(const kv_cache_desc* d, Derived* out) {
     if (d->batch < 0 || d->tokens < 1 || d->n_heads < 1 || d->head_dim < 1 || d->n_kv_heads < 0) return FUSED_PROJ_EINVAL;
     if (d->n_kv_heads > 0 && d->n_heads % d->n_kv_heads != 0) return FUSED_PROJ_EINVAL;
     if (d->page_size < 1 || d->n_pages < 1 || d->max_pages < 1) return FUSED_PROJ_EINVAL;
-    if (!(d->sm_scale >= 0.0) || !std::isfinite((float)d->sm_scale)) return FUSED_PROJ_EINVAL;
+    if (!(d->sm_scale >= 0.0) || !std::isfinite(logits_factor(*d))) return FUSED_PROJ_EINVAL;
     if (d->dtype != FUSED_PROJ_BF16) return FUSED_PROJ_EUNSUPPORTED;
     if (d->head_dim % 8 != 0 || d->head_dim > 512) return FUSED_PROJ_EUNSUPPORTED;
     if (d->page_size % 16 != 0 || d->page_size > 65536) return FUSED_PROJ_EUNSUPPORTED;
@@ -421,8 +427,10 @@ int kv_cache_attend(kv_cache_t h, const void* q, const kv_cache_storage* storage
     a.row_blocks = h->attend.row_blocks;
     a.splits = h->attend.splits;
     a.div_blocks = fp::make_fastdiv_u31((uint32_t)a.row_blocks);
-    const double scale = h->d.sm_scale > 0.0 ? h->d.sm_scale : 1.0 / std::sqrt((double)h->d.head_dim);
-    a.logit_scale = (float)(scale * 1.4426950408889634074);
+    a.logit_scale = logits_factor(h->d);
+    // 2^90, or less where the logits' factor is 2^7 or more: see lift_of in kv_attend.hip
+    const int e = a.logit_scale > 0.0f ? std::ilogb(a.logit_scale) : 0;
+    a.q_limit = 127 + 90 - (e > 6 ? e - 6 : 0);
     if (need) {
         a.part_o = static_cast<float*>(workspace);
         a.part_ml = a.part_o + (int64_t)a.splits * h->r.q_rows * h->d.head_dim;

@@ -42,10 +42,14 @@
  * exact, sums, softmax and statistics fp32, the probabilities (times v's scale) rounded to
  * bfloat16 for the second product, o rounded once. Rows of v may hold numbers of any size;
  * besides its roundings o is off by up to about 2^-90, where products with codes vanish. A
- * query row that holds a NaN, an infinity or a value of 2^90 or more gives NaN where it sees
- * any position; so does every row that sees a row kept as NaN. Positions that a token does
- * not see never reach its output, whatever their slots hold. Softmax over tiles with a running
- * maximum and sum: Milakov and Gimelshein, "Online normalizer calculation for softmax", 2018.
+ * query row that holds a NaN, an infinity or a value of 2^90 or more (2^96 divided by the
+ * greatest power of two in sm_scale log2(e), where that is less) gives NaN where it sees any
+ * position; so does every row that sees a row kept as NaN. Logits are fp32: with x[j] log2(e)
+ * of 2^127 or more a row's output is not defined. Positions that a token does not see never
+ * reach its output, whatever their slots hold. Nor do other queries, but that those of one
+ * workgroup share a power of two, whose rounding is at most 2^-39 of a key's scale in a logit.
+ * Softmax over tiles with a running maximum and sum: Milakov and Gimelshein, "Online normalizer
+ * calculation for softmax", 2018.
  *
  * Errors are the FUSED_PROJ_* codes; fused_proj_strerror() describes them. A plan only holds
  * sizes, so it may be used from several host threads and streams at once. Calls that write
@@ -74,7 +78,7 @@ typedef struct kv_cache_desc {
     int64_t page_size;   /* positions of a page, a multiple of 16 up to 65536 */
     int64_t n_pages;     /* pages of the storage, >= 1 */
     int64_t max_pages;   /* pages of a sequence (the table's width), >= 1 */
-    double sm_scale;     /* > 0, finite; 0 means 1 / sqrt(hd) */
+    double sm_scale;     /* > 0, sm_scale log2(e) below 2^128; 0 means 1 / sqrt(hd) */
 } kv_cache_desc;
 
 typedef struct kv_cache_plan *kv_cache_t;
@@ -85,7 +89,7 @@ typedef struct kv_cache_storage {
 } kv_cache_storage;
 
 /* Host-only check. FUSED_PROJ_OK, FUSED_PROJ_EINVAL (malformed: sizes, enums, KVH not
- * dividing H, a negative or non-finite sm_scale) or FUSED_PROJ_EUNSUPPORTED (not bf16,
+ * dividing H, sm_scale outside its range) or FUSED_PROJ_EUNSUPPORTED (not bf16,
  * head_dim or page_size outside the ranges above, max_pages page_size or T H of 2^30 or
  * more, b T H or b T KVH times head_dim / 8 (rounded up to a power of two) of 2^31 or more,
  * storage of 2^60 bytes or more). */

@@ -633,3 +633,39 @@ def test_attend_padding_beside_keys_of_large_scales(tokens, bits):
         qv[0, :, tokens - 1:] = junk
         qv[1, :, tokens - 2:] = junk
         assert np.array_equal(c.attend(storage, q), clean)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("tokens", [3, 40])
+@pytest.mark.parametrize("sm_power", [-3, 5, 20])
+def test_attend_large_queries_over_keys_of_large_scales(sm_power, tokens, bits):
+    """A head's queries next to the bound of what is taken (2^90, or 2^96 over the logits' factor), over keys of scales
+    of 2^14 and more: the other heads of the workgroup keep their accuracy, and the large ones have finite outputs."""
+    c = Case(bits, 2, tokens, 4, 2, 64, 16, 8, [120, 121], None, seed=16, scale=2.0 ** sm_power)
+    storage = c.dirty_storage()
+    c.fill(storage, c.random(2, 2, 128, 64) * 2.0 ** 20)
+    q = c.queries() * 2.0 ** (-23 - sm_power)                     # logits of ordinary size
+    qv = q.view(2, 4, tokens, 64)
+    largest = 89 - max(0, sm_power - 6)                           # log2(sm_scale log2 e) = sm_power + 0.53
+    power = largest - math.frexp(float(qv[:, 2].abs().max()))[1]
+    qv[:, 2] = torch.ldexp(qv[:, 2].float(), torch.tensor(power)).to(torch.bfloat16)
+    assert 2.0 ** (largest - 1) <= qv[:, 2].abs().max() < 2.0 ** largest
+    o = c.attend(storage, q)
+    want, tol = c.expected(q)
+    rest = [0, 1, 3]
+    within(o[:, :, rest], want[:, :, rest], tol[:, :, rest])
+    assert np.isfinite(o).all()
+
+
+def test_attend_query_too_large_for_its_factor_is_nan():
+    """With sm_scale log2(e) = 2^20.5 a value of 2^(96 - 20) is too large, one of half of that is not."""
+    c = Case(4, 1, 2, 4, 1, 32, 16, 2, [20], None, seed=17, scale=2.0 ** 20)
+    storage = c.dirty_storage()
+    c.fill(storage)
+    q = c.queries() * 2.0 ** -23
+    qv = q.view(4, 2, 32)
+    qv[1, 0, 4], qv[2, 1, 5] = 2.0 ** 76, -1.9375 * 2.0 ** 75
+    o = c.attend(storage, q)
+    want, tol = c.expected(q)
+    assert np.isnan(o[0, 0, 1]).all() and np.isfinite(o[0, 1]).all()
+    within(o[0, :, [0, 3]], want[0, :, [0, 3]], tol[0, :, [0, 3]])

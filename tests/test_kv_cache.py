@@ -74,3 +74,9 @@ def test_python_refusals():
         _desc(dtype=torch.float16)
     with pytest.raises(fpa.FusedProjError):
         KVCache(2, 1, 8, 20, n_pages=5, max_pages=2)
+
+
+def test_validate_bounds_the_logits_factor():
+    """sm_scale log2(e), what the kernels multiply by, has to be an fp32 number."""
+    assert validate_kv_cache(_desc(sm_scale=2.3e38)) == fpa.OK
+    assert validate_kv_cache(_desc(sm_scale=2.4e38)) == fpa.EINVAL
