@@ -391,3 +391,54 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
         ln(x, gamma, beta, out=(torch.empty_like(x), None))
     with pytest.raises(ValueError):
         ln.backward(x, gamma, torch.zeros((2, 10), device=DEV), dy)
+
+
+# (layout, dtype, batch, channels, tokens): more strips or rows than twice the workgroups, the last turn of some of them only
+TURNS = [
+    # strips of 32 (bf16) or 16 tokens, 1024, 512 or 256 workgroups; slabs that end with a strip, and ones that do not
+    ("channels_first", B, 70, 40, 1000), ("channels_first", B, 70, 40, 1024), ("channels_first", B, 70, 384, 1000),
+    ("channels_first", F, 40, 200, 1000), ("channels_first", F, 40, 200, 1008), ("channels_first", F, 40, 384, 1001),
+    ("channels_first", B, 40, 768, 1000), ("channels_first", B, 40, 700, 1024), ("channels_first", F, 20, 513, 1000),
+    ("channels_first", B, 20, 1408, 1000), ("channels_first", B, 20, 1030, 1024), ("channels_first", F, 20, 800, 600),
+    # more channels than a workgroup holds; slabs shorter than a strip
+    ("channels_first", B, 20, 1600, 1000), ("channels_first", F, 12, 1700, 1008), ("channels_first", B, 700, 24, 11),
+    # 8, 2 and 1 rows a workgroup, 512 of them
+    ("tokens_last", B, 1, 40, 10001), ("tokens_last", B, 1, 2048, 9001), ("tokens_last", B, 3, 1387, 3001),
+    ("tokens_last", F, 1, 1000, 9001), ("tokens_last", B, 1, 4096, 2501), ("tokens_last", B, 1, 4099, 2501),
+    ("tokens_last", B, 1, 8192, 2100), ("tokens_last", F, 1, 1387, 2501), ("tokens_last", F, 1, 4096, 2501),
+    ("tokens_last", B, 1, 8200, 1300), ("tokens_last", B, 1, 16385, 1100), ("tokens_last", F, 1, 4100, 1300),
+    ("tokens_last", F, 1, 9000, 1100), ("tokens_last", F, 1, 20000, 1100),
+]
+
+
+@pytest.mark.parametrize("case", TURNS, ids=[f"{c[0][:2]}_{'bf16' if c[1] is B else 'f32'}_b{c[2]}_c{c[3]}_s{c[4]}" for c in TURNS])
+def test_backward_of_workgroups_that_take_several_turns(case):
+    """x, dy and the tokens' means are whole numbers, their rstds powers of two: every term of dgamma and dbeta is a multiple
+    of a half below 2^7, and a thread adds fewer than 2^15 of them: below 2^23, every partial sum is exact in 24 bits. A
+    strip or row that is lost, doubled or swapped shows in full."""
+    print(f"[case] layer_norm turns {case}", flush=True)
+    layout, dtype, batch, channels, tokens = case
+    first = layout == "channels_first"
+    g = torch.Generator(device=DEV).manual_seed(21)
+    whole = lambda low, high, *s: torch.randint(low, high + 1, s, generator=g, device=DEV).to(torch.float64)
+    shape = (batch, channels, tokens) if first else (batch, tokens, channels)
+    x, dy = whole(-8, 8, *shape), whole(-4, 5, *shape)     # dy's mean is a half: whole turns weigh in
+    mean, rstd = whole(-2, 3, batch, tokens), 2.0 ** whole(-1, 1, batch, tokens)
+    gamma = (1.0 + 0.3 * torch.randn(channels, generator=g, device=DEV)).to(dtype)
+    ln = LayerNorm(shape, torch.empty(shape, device="meta").stride(), layout, dtype)
+    nan = lambda s: torch.full(s, float("nan"), dtype=dtype, device=DEV)
+    out = (nan(shape), nan((channels,)), nan((channels,)))
+    workspace = torch.full((ln.workspace_bytes() // 4,), float("nan"), device=DEV)
+    stats = torch.stack([mean.reshape(-1), rstd.reshape(-1)]).float()
+    dx, dgamma, dbeta = ln.backward(x.to(dtype), gamma, stats, dy.to(dtype), out=out, workspace=workspace)
+    axis, other = (1, (0, 2)) if first else (2, (0, 1))
+    mean, rstd = mean.unsqueeze(axis), rstd.unsqueeze(axis)
+    xhat = (x - mean) * rstd
+    assert torch.equal(dgamma, (dy * xhat).sum(other).to(torch.float32).to(dtype))
+    assert torch.equal(dbeta, dy.sum(other).to(torch.float32).to(dtype))
+    gd = dy * gamma.double().view([1, -1, 1] if first else [1, 1, -1])
+    c1, c2 = gd.mean(axis, keepdim=True), (gd * xhat).mean(axis, keepdim=True)
+    want = rstd * (gd - c1 - xhat * c2)
+    tol = K * U * (gd.abs().mean(axis, keepdim=True) + xhat.abs() * (gd * xhat).abs().mean(axis, keepdim=True))
+    tol = HALF[dtype] * want.abs() + rstd * (tol + 8 * U * (gd.abs() + c1.abs() + (xhat * c2).abs()))
+    assert ((dx.double() - want).abs() <= tol).all()
