@@ -613,7 +613,8 @@ template <typename T>
 __global__ __launch_bounds__(1024) void layer_norm_columns_kernel(const float* partial, T* dgamma, T* dbeta, int C,
                                                                   int parts) {
     __shared__ double red[32][33];
-    const int col = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
+    // rows of kMostBlocks; the last workgroups may be past the columns, 2^30 + 2^25 at most
+    const int col = (int)(blockIdx.y * gridDim.x + blockIdx.x) * 32 + (int)(threadIdx.x & 31), r = threadIdx.x >> 5;
     double s = 0.0;
     if (col < 2 * C) {
         int p = r;
@@ -791,9 +792,12 @@ NormArgs base_args(const layer_norm_plan* h, const void* x, const void* gamma) {
     return a;
 }
 
+dim3 grid_of(int64_t blocks) {
+    const unsigned x = (unsigned)(blocks < kMostBlocks ? blocks : kMostBlocks);
+    return dim3(x, (unsigned)((blocks + x - 1) / x));
+}
 void launch(void (*kernel)(NormArgs), int64_t grid, int block, const NormArgs& a, hipStream_t st) {
-    const unsigned x = (unsigned)(grid < kMostBlocks ? grid : kMostBlocks), y = (unsigned)((grid + x - 1) / x);
-    hipLaunchKernelGGL(kernel, dim3(x, y), dim3(block), 0, st, a);
+    hipLaunchKernelGGL(kernel, grid_of(grid), dim3(block), 0, st, a);
 }
 
 template <typename T, bool TAIL>
@@ -948,7 +952,7 @@ int layer_norm_backward(layer_norm_t h, const void* x, const void* gamma, const 
         if (rc2) return rc2;
     }
     // with no tokens there are no parts, and the sums are 0
-    const dim3 grid((unsigned)((2 * r.C + 31) / 32));
+    const dim3 grid = grid_of((2 * r.C + 31) / 32);
     if (h->d.dtype == FUSED_PROJ_BF16)
         hipLaunchKernelGGL((layer_norm_columns_kernel<__bf16>), grid, dim3(1024), 0, st,
                            static_cast<const float*>(workspace), static_cast<__bf16*>(dgamma),

@@ -442,3 +442,35 @@ def test_backward_of_workgroups_that_take_several_turns(case):
     tol = K * U * (gd.abs().mean(axis, keepdim=True) + xhat.abs() * (gd * xhat).abs().mean(axis, keepdim=True))
     tol = HALF[dtype] * want.abs() + rstd * (tol + 8 * U * (gd.abs() + c1.abs() + (xhat * c2).abs()))
     assert ((dx.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("tokens", [0, 1])
+def test_more_channels_than_one_dimension_of_a_grid_has_columns(tokens):
+    """2^26 + 5 channels: dgamma and dbeta are 2^27 + 10 columns, more than 2^32 threads. With one token they are dy xhat
+    and dy: a few roundings and the storage type's; with none 0."""
+    C = (1 << 26) + 5
+    g = torch.Generator(device=DEV).manual_seed(22)
+    rand = lambda *s: torch.randn(s, generator=g, device=DEV).to(B)
+    x, dy, gamma = rand(1, C, tokens), rand(1, C, tokens), rand(C)
+    x.mul_(2.0), dy.add_(1.0)
+    ln = LayerNorm.for_tensor(x, "channels_first")
+    nan = lambda *s: torch.full(s, float("nan"), dtype=B, device=DEV)
+    out = (nan(1, C, tokens), nan(C), nan(C))
+    stats = torch.tensor([[0.25], [0.5]], device=DEV)[:, :tokens].contiguous()
+    dx, dgamma, dbeta = ln.backward(x, gamma, stats, dy, out=out)
+    torch.cuda.synchronize()
+    if tokens == 0:
+        assert not dgamma.any() and not dbeta.any()
+        return
+    xhat, d = ((x.double() - 0.25) * 0.5).view(-1), dy.double().view(-1)
+    want = d * xhat
+    assert ((dgamma.double() - want).abs() <= (HALF[B] + 8 * U) * want.abs()).all()
+    assert torch.equal(dbeta, dy.view(-1))
+    gd = d * gamma.double()
+    c1, c2 = gd.mean(), (gd * xhat).mean()
+    want = 0.5 * (gd - c1 - xhat * c2)
+    # 2^18 terms a thread of the means, then the lanes' and waves'
+    k = (C // 256 + 30) * U
+    tol = HALF[B] * want.abs() + 0.5 * (k * (gd.abs().mean() + xhat.abs() * (gd * xhat).abs().mean())
+                                        + 8 * U * (gd.abs() + c1.abs() + (xhat * c2).abs()))
+    assert ((dx.double().view(-1) - want).abs() <= tol).all()
