@@ -6,6 +6,8 @@
  * tokens of sequence i; the last counts[i] of them (0 <= counts[i] <= T; T where counts is
  * NULL) are the step's own: token s < counts[i] of the step is at position
  * lengths[i] - counts[i] + s of the sequence. Tokens s >= counts[i] are padding.
+ * Rotations are the caller's: a projection's or a split + RoPE's plan rotates from one
+ * pos_offset, so sequences at different positions take a plan each.
  *
  * Format. A row is the hd values x of one token of one k/v head, in k or in v:
  *
