@@ -28,9 +28,9 @@
 // operand shares. V's operand needs 8 positions of one element in a lane: a lane reads the
 // same few bytes of 8 positions and pairs them up with byte permutes.
 //
-// Measured, 4 bits, 32 heads on 8 x 128: 63 sequences of 8191 positions, one token each, 105 us
-// (5.3 TB/s, a large copy's rate; 42% of the vector pipes' time); of 2500 to 8191 positions 79
-// us; 2 x 1024 tokens over 4096 positions 185 us (650 TFLOP/s; a large bf16 product reaches
+// Measured, 4 bits, 32 heads on 8 x 128: 63 sequences of 8191 positions, one token each, 106 us
+// (5.2 TB/s, a large copy's rate); of 2500 to 8191 positions 80 us (48% of the vector pipes'
+// time); 2 x 1024 tokens over 4096 positions 180 us (670 TFLOP/s; a large bf16 product reaches
 // 1209).
 #include <cmath>
 
@@ -483,7 +483,9 @@ __device__ __forceinline__ Share share_of(const CacheArgs& a) {
 // rows and take different positions, each by itself; at the end they are put together in
 // LDS. Bound by the cache's bytes: the next tile is loaded while one is taken.
 //
-// Waves a SIMD: as many as the registers of two tiles and the output leave without spills.
+// Waves a SIMD: as many as the registers of two tiles and the output leave; 8 bits with heads of
+// 128 and two row tiles spill 20 bytes a lane at two waves, 8 bits with heads of 256 take
+// accumulation registers besides, and one wave.
 template <int D, int BITS, int R>
 constexpr int kStepWaves = D * BITS > 1536 ? 1 : D * BITS <= 512 && R == 1 && Shape<D, BITS>::D1 == 0 ? 3 : 2;
 
@@ -846,7 +848,8 @@ __global__ __launch_bounds__(256) void kv_attend_join_kernel(CacheArgs a) {
 }
 
 // Rows of a wave of the chunk kernel (in tiles of 16), and sets of operands (of 64 (4 D + 16)
-// bytes each): as two workgroups a CU leave registers and LDS.
+// bytes each): as two workgroups a CU leave registers and LDS (8 bits with heads of 128 spill
+// 40 bytes a lane).
 constexpr int kChunkWaves = 4;
 constexpr int chunk_tiles(int64_t d) { return d <= 128 ? 2 : 1; }
 constexpr int chunk_sets(int64_t d) { return d <= 128 ? 2 : 1; }
@@ -879,9 +882,10 @@ bool plan_attend(const kv_cache_desc& d, int64_t kvh, AttendPlan* out) {
     // enough workgroups to fill the card, with parts long enough to be worth their queries and
     // their join. Parts of one size for all sequences measured slower (104 us instead of 84
     // for 64 sequences of 2500 to 8191 positions). Few rows: half as many workgroups again
-    // where parts are longer than 2048 positions, so that long sequences end together with
-    // short ones (63 sequences up to 8191: 83 -> 79 us); where parts are shorter, their
-    // number costs more than it gives (24 of up to 3333: 22.5 -> 23.2 us).
+    // where parts are longer than 2048 positions (63 sequences up to 8191: 2 parts 83 us, 3 parts
+    // 79), not where they are shorter (24 of up to 3333: 4 parts 22.5 us, 6 parts 23.2). The
+    // rule does not count the workgroups that are resident, three a CU for both: 768, of which
+    // these are 1.3 and 2.0, 1.5 and 2.25 rounds.
     const int64_t positions = d.max_pages * d.page_size, least = p.chunk ? 512 : 256;
     const auto parts = [&](int64_t want) { return (want + heads * p.row_blocks - 1) / (heads * p.row_blocks); };
     const int64_t want = p.chunk ? 512 : positions > 2048 * parts(1024) ? 1536 : 1024;

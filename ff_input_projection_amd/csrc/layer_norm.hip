@@ -3,8 +3,10 @@
 //
 // The op moves bytes: forward reads x and writes y, backward reads x and dy and writes dx,
 // with about 10 and 20 VALU operations a value where the memory rate allows 28 and 42. Each
-// tensor is touched once: a token's channels stay in registers (as stored, unpacked again
-// for each use) between the sums over them and the output that needs the sums.
+// tensor is touched once, where a row or strip fits a workgroup's registers: a token's channels
+// stay there (as stored, unpacked again for each use) between the sums over them and the output
+// that needs the sums. Channels-first, more than 1536 channels or slabs shorter than a strip do
+// not, and are read again for each use.
 //
 // Token-major rows: TPR threads (a wave, or a workgroup of 256 or 1024) hold a row, NCH
 // 16-byte pieces each. Channels-first: a workgroup holds a strip of TL * V tokens with all
@@ -17,7 +19,9 @@
 //
 // Measured (a large copy reaches 5.2 TB/s): forward 24 x 768 x 1024 bf16 channels-first 16.6 us
 // (4.6 TB/s), 3063 rows of 1387 fp32 8.6 us (4.0 TB/s); backward 16384 rows of 768 bf16 16 us
-// (4.7 TB/s), 24 x 1408 x 1024 bf16 channels-first 57 us (3.6 TB/s); column sums 3 to 5 us.
+// (4.7 TB/s), 24 x 1408 x 1024 bf16 channels-first 57 us (3.6 TB/s); column sums 3 to 5 us. Rows
+// that leave a wave mostly idle, 131072 of 24 bf16: 33 us (0.4 TB/s), backward 41; strips that
+// are read again, 24 x 2048 x 1024 bf16: 69 us (2.9 TB/s), backward 113.
 #include <hip/hip_runtime.h>
 
 #include <cmath>

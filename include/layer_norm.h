@@ -19,7 +19,8 @@
  * Sums, statistics and every intermediate value are fp32 (the last stage of dgamma and
  * dbeta is a 64-bit sum); each output is rounded once to the storage type. Results do not
  * depend on timing: no atomics. NaN and infinities reach their own token's y and dx, and
- * their channel's dgamma and dbeta, as the formulas give them.
+ * their channel's dgamma and dbeta, as the formulas give them. Sums beyond fp32's range are
+ * infinite: with a value 2^64 away from the mean the variance is, and rstd 0.
  *
  * Memory: the caller owns every device buffer. Errors are the FUSED_PROJ_* codes;
  * fused_proj_strerror() describes them. A plan only holds sizes, so it may be used from
