@@ -414,8 +414,11 @@ __device__ __forceinline__ uint32_t find_rows(Rows<D, BITS, R>& w, u32x4 (&raw)[
         uint32_t mine = 0;
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
-            // padding sees nothing: what lies there takes no part, in the lift neither
-            raw[r][j] = w.last[r] >= 0 ? *reinterpret_cast<const u32x4*>(q + j * 8) : u32x4{0, 0, 0, 0};
+            raw[r][j] = w.real[r] ? *reinterpret_cast<const u32x4*>(q + j * 8) : u32x4{0, 0, 0, 0};
+            // padding sees nothing: what lies there takes no part, in the lift neither (behind the load,
+            // which does not wait for the sequence's lengths)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) raw[r][j][i] = w.last[r] >= 0 ? raw[r][j][i] : 0u;
 #pragma unroll
             for (int i = 0; i < 4; ++i) mine = max(mine, max((raw[r][j][i] >> 7) & 0xFFu, (raw[r][j][i] >> 23) & 0xFFu));
         }
