@@ -18,9 +18,9 @@ import os
 
 import torch
 
-__all__ = ["FusedProjection", "FusedProjError", "SplitRope", "LayerNorm", "KVCache", "load_library",
-           "LIB_PATH", "EXPORTED_SYMBOLS", "LAYER_NORM_SYMBOLS", "KV_CACHE_SYMBOLS", "Desc", "SplitRopeDesc",
-           "LayerNormDesc", "KVCacheDesc"]
+__all__ = ["FusedProjection", "FusedProjError", "SplitRope", "LayerNorm", "KVCache", "Rope", "load_library",
+           "LIB_PATH", "EXPORTED_SYMBOLS", "LAYER_NORM_SYMBOLS", "KV_CACHE_SYMBOLS", "ROPE_SYMBOLS", "Desc", "SplitRopeDesc",
+           "LayerNormDesc", "KVCacheDesc", "RopeDesc"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libfused_proj.so")
@@ -37,6 +37,9 @@ LAYER_NORM_SYMBOLS = ["layer_norm_validate", "layer_norm_create", "layer_norm_ru
 # include/kv_cache.h
 KV_CACHE_SYMBOLS = ["kv_cache_validate", "kv_cache_create", "kv_cache_storage_bytes", "kv_cache_write", "kv_cache_read",
                     "kv_cache_attend_workspace_size", "kv_cache_attend", "kv_cache_destroy"]
+# include/rope.h
+ROPE_SYMBOLS = ["rope_validate", "rope_create", "rope_split", "rope_split_backward", "rope_rotate",
+                "rope_rotate_backward", "rope_destroy"]
 
 OK, EINVAL, EUNSUPPORTED, EALIGN, EALIAS, EHIP, ESCRATCH = 0, -1, -2, -3, -4, -5, -6
 BF16, F32 = 0, 1
@@ -96,6 +99,17 @@ class KVCacheDesc(ctypes.Structure):
 class KVCacheStorage(ctypes.Structure):
     """Mirror of ``kv_cache_storage``."""
     _fields_ = [(name, ctypes.c_void_p) for name in ("k_codes", "k_params", "v_codes", "v_params")]
+
+
+class RopeDesc(ctypes.Structure):
+    """Mirror of ``rope_desc``."""
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("qkv_order", ctypes.c_int32), ("batch", ctypes.c_int64), ("tokens", ctypes.c_int64),
+        ("n_heads", ctypes.c_int64), ("n_kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+        ("rope_dims", ctypes.c_int64), ("pairs", ctypes.c_int32), ("scaling", ctypes.c_int32),
+        ("rope_base", ctypes.c_double), ("factor", ctypes.c_double), ("low_turns", ctypes.c_double),
+        ("high_turns", ctypes.c_double), ("original_tokens", ctypes.c_int64), ("magnitude", ctypes.c_double),
+    ]
 
 
 class FusedProjError(RuntimeError):
@@ -168,6 +182,13 @@ def load_library():
     lib.kv_cache_attend.argtypes = [vp, vp, storage_p, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
     lib.kv_cache_destroy.argtypes = [vp]
     for name in KV_CACHE_SYMBOLS:
+        getattr(lib, name).restype = ctypes.c_int
+    lib.rope_validate.argtypes = [ctypes.POINTER(RopeDesc)]
+    lib.rope_create.argtypes = [ctypes.POINTER(RopeDesc), ctypes.POINTER(vp)]
+    for name in ("rope_split", "rope_split_backward", "rope_rotate", "rope_rotate_backward"):
+        getattr(lib, name).argtypes = [vp] * 7
+    lib.rope_destroy.argtypes = [vp]
+    for name in ROPE_SYMBOLS:
         getattr(lib, name).restype = ctypes.c_int
     lib.fused_proj_mfma_ceiling.argtypes = [ctypes.c_int, ctypes.c_uint, vp, ctypes.c_size_t, vp,
                                             ctypes.POINTER(ctypes.c_double)]
@@ -551,3 +572,4 @@ class SplitRope:
 
 from .kv_cache import KVCache, make_kv_cache_desc, validate_kv_cache  # noqa: E402
 from .layer_norm import LayerNorm, make_layer_norm_desc, validate_layer_norm  # noqa: E402
+from .rope import Rope, make_rope_desc, validate_rope  # noqa: E402
