@@ -18,9 +18,11 @@ import os
 
 import torch
 
-__all__ = ["FusedProjection", "FusedProjError", "SplitRope", "LayerNorm", "KVCache", "Rope", "load_library",
-           "LIB_PATH", "EXPORTED_SYMBOLS", "LAYER_NORM_SYMBOLS", "KV_CACHE_SYMBOLS", "ROPE_SYMBOLS", "Desc", "SplitRopeDesc",
-           "LayerNormDesc", "KVCacheDesc", "RopeDesc"]
+__all__ = ["FusedProjection", "FusedProjError", "SplitRope", "LayerNorm", "KVCache", "Rope", "PromptAttention",
+           "load_library",
+           "LIB_PATH", "EXPORTED_SYMBOLS", "LAYER_NORM_SYMBOLS", "KV_CACHE_SYMBOLS", "ROPE_SYMBOLS",
+           "PROMPT_ATTENTION_SYMBOLS", "Desc", "SplitRopeDesc", "LayerNormDesc", "KVCacheDesc", "RopeDesc",
+           "PromptAttentionDesc"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libfused_proj.so")
@@ -40,6 +42,9 @@ KV_CACHE_SYMBOLS = ["kv_cache_validate", "kv_cache_create", "kv_cache_storage_by
 # include/rope.h
 ROPE_SYMBOLS = ["rope_validate", "rope_create", "rope_split", "rope_split_backward", "rope_rotate",
                 "rope_rotate_backward", "rope_destroy"]
+# include/prompt_attention.h
+PROMPT_ATTENTION_SYMBOLS = ["prompt_attention_validate", "prompt_attention_create", "prompt_attention_workspace_size",
+                            "prompt_attention_run", "prompt_attention_backward", "prompt_attention_destroy"]
 
 OK, EINVAL, EUNSUPPORTED, EALIGN, EALIAS, EHIP, ESCRATCH = 0, -1, -2, -3, -4, -5, -6
 BF16, F32 = 0, 1
@@ -109,6 +114,16 @@ class RopeDesc(ctypes.Structure):
         ("rope_dims", ctypes.c_int64), ("pairs", ctypes.c_int32), ("scaling", ctypes.c_int32),
         ("rope_base", ctypes.c_double), ("factor", ctypes.c_double), ("low_turns", ctypes.c_double),
         ("high_turns", ctypes.c_double), ("original_tokens", ctypes.c_int64), ("magnitude", ctypes.c_double),
+    ]
+
+
+class PromptAttentionDesc(ctypes.Structure):
+    """Mirror of ``prompt_attention_desc``."""
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("causal", ctypes.c_int32), ("batch", ctypes.c_int64), ("tokens", ctypes.c_int64),
+        ("n_heads", ctypes.c_int64), ("n_kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+        ("sequences", ctypes.c_int64), ("q_strides", ctypes.c_int64 * 3), ("k_strides", ctypes.c_int64 * 3),
+        ("v_strides", ctypes.c_int64 * 3), ("sm_scale", ctypes.c_double),
     ]
 
 
@@ -189,6 +204,14 @@ def load_library():
         getattr(lib, name).argtypes = [vp] * 7
     lib.rope_destroy.argtypes = [vp]
     for name in ROPE_SYMBOLS:
+        getattr(lib, name).restype = ctypes.c_int
+    lib.prompt_attention_validate.argtypes = [ctypes.POINTER(PromptAttentionDesc)]
+    lib.prompt_attention_create.argtypes = [ctypes.POINTER(PromptAttentionDesc), ctypes.POINTER(vp)]
+    lib.prompt_attention_workspace_size.argtypes = [vp, size_p, size_p]
+    lib.prompt_attention_run.argtypes = [vp] * 8 + [ctypes.c_size_t, vp]
+    lib.prompt_attention_backward.argtypes = [vp] * 12 + [ctypes.c_size_t, vp]
+    lib.prompt_attention_destroy.argtypes = [vp]
+    for name in PROMPT_ATTENTION_SYMBOLS:
         getattr(lib, name).restype = ctypes.c_int
     lib.fused_proj_mfma_ceiling.argtypes = [ctypes.c_int, ctypes.c_uint, vp, ctypes.c_size_t, vp,
                                             ctypes.POINTER(ctypes.c_double)]
@@ -572,4 +595,5 @@ class SplitRope:
 
 from .kv_cache import KVCache, make_kv_cache_desc, validate_kv_cache  # noqa: E402
 from .layer_norm import LayerNorm, make_layer_norm_desc, validate_layer_norm  # noqa: E402
+from .prompt_attention import PromptAttention, make_prompt_attention_desc, validate_prompt_attention  # noqa: E402
 from .rope import Rope, make_rope_desc, validate_rope  # noqa: E402

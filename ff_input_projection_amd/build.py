@@ -22,7 +22,8 @@ SOURCES = [os.path.join(CSRC, "fused_proj_api.cpp"), os.path.join(CSRC, "fused_p
            os.path.join(CSRC, "fused_proj_fast.hip"), os.path.join(CSRC, "split_rope.hip"),
            os.path.join(CSRC, "fused_proj_bwd.hip"), os.path.join(CSRC, "mfma_ceiling.hip"),
            os.path.join(CSRC, "layer_norm.hip"), os.path.join(CSRC, "kv_cache.hip"), os.path.join(CSRC, "kv_attend.hip"),
-           os.path.join(CSRC, "rope.hip")]
+           os.path.join(CSRC, "rope.hip"), os.path.join(CSRC, "prompt_attention.hip"),
+           os.path.join(CSRC, "prompt_attention_bwd.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",

@@ -35,7 +35,7 @@ struct Slot {
     std::vector<Spec> specs;
     int64_t bytes = 0;
 };
-constexpr int kMostArgs = 12, kMostStorage = 8;
+constexpr int kMostArgs = 14, kMostStorage = 8;
 struct Plan {
     uintptr_t fn, handle;
     at::Device device;
@@ -159,6 +159,9 @@ int invoke(uintptr_t fn, int n, const uintptr_t* a) {
         case 11:
             return CALL(U, U, U, U, U, U, U, U, U, U, U)(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9],
                                                          a[10]);
+        case 14:
+            return CALL(U, U, U, U, U, U, U, U, U, U, U, U, U, U)(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9],
+                                                                  a[10], a[11], a[12], a[13]);
     }
 #undef CALL
     return INT32_MIN;
