@@ -65,6 +65,7 @@ struct Span {
     int32_t first, last;
 };
 constexpr int32_t kNone = 0x7FFFFFFF;
+__device__ __forceinline__ bool sees(Span s, int at) { return at >= s.first && at <= s.last && s.first != kNone; }
 
 // LDS of find_spans.
 template <int BM>
@@ -161,12 +162,6 @@ struct Rows {
         const i16x4 lo = turned_half(base, t, s, 0), hi = turned_half(base, t, s, 1);
         return __builtin_bit_cast(bf16x8, i16x8{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w});
     }
-    // The 4 elements of a row that values 4 i .. 4 i + 3 of a lane of Y^T's tile t are sums of.
-    static __device__ __forceinline__ u32x2 four(unsigned tile, int row, int t, int i) {
-        const int c = 4 * t + i;
-        const unsigned at = tile + row * BYTES + (c / G * G + ((c % G) ^ swizzle(row))) * 16 + ((threadIdx.x & 63) >> 5) * 8;
-        return *(const __attribute__((address_space(3))) u32x2*)(size_t)at;
-    }
 };
 
 // The same address in SGPRs.
@@ -232,38 +227,42 @@ __device__ __forceinline__ void load_rows(bf16x8 (&to)[D / 16], const char* row,
 // The rows of a lane's 16 values of a 32 x 32 product.
 __device__ __forceinline__ int value_row(int i) { return (i & 3) + 8 * (i >> 2) + 4 * ((threadIdx.x & 63) >> 5); }
 
-// Values 8 s .. 8 s + 7 of X as operand B of Y^T.
-__device__ __forceinline__ bf16x8 as_operand(const f32x16& x, int s) {
-    bf16x8 o;
+// X, rounded, as operands B of Y^T.
+template <int NB>
+__device__ __forceinline__ void to_operands(bf16x8 (&o)[2 * NB], const f32x16 (&x)[NB]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = (__bf16)x[8 * s + i];
-    return o;
+    for (int s = 0; s < 2 * NB; ++s)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[s][i] = (__bf16)x[s >> 1][8 * (s & 1) + i];
 }
 
-__device__ __forceinline__ bool not_finite(uint32_t bf16) { return (bf16 & 0x7F80u) == 0x7F80u; }
+// bf16 pairs whose exponent is the largest (infinities and NaN) as masks of 16 bits.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+    const uint32_t up = (w & 0x7F807F80u) + 0x00800080u;   // bit 15 of a half: its exponent was 255
+    return ((up >> 15) & 0x00010001u) * 0xFFFFu;
+}
 __device__ __forceinline__ bf16x8 only_finite(bf16x8 x) {
     u32x4 w = __builtin_bit_cast(u32x4, x);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (not_finite(w[i])) w[i] &= 0xFFFF0000u;
-        if (not_finite(w[i] >> 16)) w[i] &= 0x0000FFFFu;
-    }
+    for (int i = 0; i < 4; ++i) w[i] &= ~not_finite(w[i]);
     return __builtin_bit_cast(bf16x8, w);
 }
 
-// X = A B^T for NB blocks of 32 rows of the tile whose plain base is given. Operands are read two
-// steps ahead of their products, in groups that the compiler keeps apart: it would read them all at
+// X = A B^T for NB blocks of 32 rows of the tile whose plain base is given; b(kk): operand B. Operands are read ahead of
+// their products, in groups (of J steps) that the compiler keeps apart: it would read them all at
 // once else, into registers that there are not.
-template <int D, int NB>
-__device__ __forceinline__ void product(f32x16 (&x)[NB], const bf16x8 (&b)[D / 16], unsigned base) {
+template <int D, int NB, int J, typename B>
+__device__ __forceinline__ void product(f32x16 (&x)[NB], const B& b, unsigned base) {
     using R = Rows<D>;
     constexpr int K = D / 16;
-    bf16x8 a[2][2][NB];
+    bf16x8 a[2][J][NB], w[2][J];
     const auto read = [&](int k) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < J; ++j) {
+            w[(k / J) & 1][j] = b(k + j);
 #pragma unroll
-            for (int u = 0; u < NB; ++u) a[(k >> 1) & 1][j][u] = R::plain(base, u, k + j);
+            for (int u = 0; u < NB; ++u) a[(k / J) & 1][j][u] = R::plain(base, u, k + j);
+        }
     };
 #pragma unroll
     for (int u = 0; u < NB; ++u)
@@ -271,79 +270,85 @@ __device__ __forceinline__ void product(f32x16 (&x)[NB], const bf16x8 (&b)[D / 1
         for (int i = 0; i < 16; ++i) x[u][i] = 0.0f;
     read(0);
 #pragma unroll
-    for (int k = 0; k < K; k += 2) {
-        if (k + 2 < K) read(k + 2);
+    for (int k = 0; k < K; k += J) {
+        if (k + J < K) read(k + J);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < J; ++j)
 #pragma unroll
             for (int u = 0; u < NB; ++u)
-                x[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[(k >> 1) & 1][j][u], b[k + j], x[u], 0, 0, 0);
+                x[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[(k / J) & 1][j][u], w[(k / J) & 1][j], x[u], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
     }
 }
 
-// Y^T += A'^T X for the tile of 32 NB rows at `tile`, its turned base given.
+// Y^T += A'^T X for the tile of 32 NB rows whose turned base is given; C tiles of Y^T a group.
 // Where the mask hides some of the tile's rows from some of the wave's (`edge`), their values in X
-// are 0, but 0 times an infinity or NaN is NaN: a product of the tile with zeros tells whether it
-// holds any. Then they are left out, and added one by one to the rows that see them.
-template <int D, int NB, typename Sees>
-__device__ __forceinline__ void add_turned(f32x16 (&y)[D / 32], const f32x16 (&x)[NB], unsigned base, unsigned tile, bool edge,
-                                           Sees sees) {
+// are 0, but 0 times an infinity or NaN is NaN. A product of the tile with zeros tells whether it
+// holds any; then they are left out here, and true is returned: add_left_out has to follow.
+template <int D, int NB, int C>
+__device__ __forceinline__ bool add_turned(f32x16 (&y)[D / 32], const bf16x8 (&x)[2 * NB], unsigned base, bool edge) {
     using R = Rows<D>;
-    constexpr int T = D / 32, S = 2 * NB;
-    bf16x8 a[2][T];
-    const auto read = [&](int s) {
+    constexpr int T = D / 32, S = 2 * NB, P = T / C;   // P groups a step
+    static_assert(P * C == T, "whole groups");
+    bf16x8 a[2][C];
+    const auto read = [&](int i) {
 #pragma unroll
-        for (int t = 0; t < T; ++t) a[s & 1][t] = R::turned(base, t, s);
+        for (int c = 0; c < C; ++c) a[i & 1][c] = R::turned(base, i % P * C + c, i / P);
     };
     bool all_finite = true;
     if (edge) {
         f32x4 probe = {0, 0, 0, 0};
         const bf16x8 zeros = {};
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            read(s);
+        for (int i = 0; i < S * P; ++i) {
+            read(i);
 #pragma unroll
-            for (int t = 0; t < T; ++t) probe = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[s & 1][t], zeros, probe, 0, 0, 0);
+            for (int c = 0; c < C; ++c) probe = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i & 1][c], zeros, probe, 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
         // a NaN in a row of A makes the product's whole row NaN: each lane has 4 of its rows
         all_finite = !__any(probe[0] != 0.0f || probe[1] != 0.0f || probe[2] != 0.0f || probe[3] != 0.0f);
     }
-    if (all_finite) {
-        read(0);
+    read(0);
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            if (s + 1 < S) read(s + 1);
-            const bf16x8 b = as_operand(x[s >> 1], s & 1);
+    for (int i = 0; i < S * P; ++i) {
+        if (i + 1 < S * P) read(i + 1);
+        if (!all_finite) {
+            asm volatile("");   // a branch, not selects
 #pragma unroll
-            for (int t = 0; t < T; ++t) y[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[s & 1][t], b, y[t], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
+            for (int c = 0; c < C; ++c) a[i & 1][c] = only_finite(a[i & 1][c]);
         }
-    } else {
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const bf16x8 b = as_operand(x[s >> 1], s & 1);
+        for (int c = 0; c < C; ++c)
+            y[i % P * C + c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i & 1][c], x[i / P], y[i % P * C + c], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    return !all_finite;
+}
+
+// What add_turned left out of the tiles of BN rows from `low` on, up to row `high`: their infinities and
+// NaN (as NaN, with AS_NAN), straight from memory, added to the rows that see them. `rows`: row 0; `edge(p)`: whether tile p was
+// one. Behind the loop over the tiles, and not in it, where it would cost every wave registers.
+template <int D, int BN, bool AS_NAN, typename Edge>
+__device__ __forceinline__ void add_left_out(f32x16 (&y)[D / 32], const char* rows, uint32_t stride, int low, int high, Span mine,
+                                             int hd, Edge edge) {
+    const int h = (threadIdx.x & 63) >> 5;
+#pragma unroll 1
+    for (int p = low; p <= high; p += BN) {
+        if (!edge(p)) continue;
+#pragma unroll 1
+        for (int row = p; row < p + BN && row <= high; ++row) {
+            const bool see = sees(mine, row);
 #pragma unroll
-            for (int t = 0; t < T; ++t) {
-                y[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(only_finite(R::turned(base, t, s)), b, y[t], 0, 0, 0);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        }
-        for (int row = 0; row < 32 * NB; ++row) {
-            const bool see = sees(row);
+            for (int i = 0; i < D / 8; ++i) {
+                u32x2 e = {0, 0};
+                if (8 * i < hd) e = *reinterpret_cast<const u32x2*>(rows + (int64_t)row * stride + 16 * i + 8 * h);
 #pragma unroll
-            for (int t = 0; t < T; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const u32x2 e = R::four(tile, row, t, i);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t bits = k & 1 ? e[k >> 1] & 0xFFFF0000u : e[k >> 1] << 16;
-                        if (see && not_finite(bits >> 16)) y[t][4 * i + k] += __uint_as_float(bits);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t bits = k & 1 ? e[k >> 1] & 0xFFFF0000u : e[k >> 1] << 16;
+                    if (see && (bits & 0x7F800000u) == 0x7F800000u) y[i >> 2][4 * (i & 3) + k] += __uint_as_float(AS_NAN ? 0x7FC00000u : bits);
                 }
+            }
         }
     }
 }
@@ -394,7 +399,6 @@ __device__ __forceinline__ WaveSight wave_sight(Span s) {
     w.high = __builtin_amdgcn_readlane(s.last, b);
     return w;
 }
-__device__ __forceinline__ bool sees(Span s, int at) { return at >= s.first && at <= s.last && s.first != kNone; }
 
 }  // namespace dev
 }  // namespace fp

@@ -78,18 +78,19 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_kerne
         k_loads.issue(k + (int64_t)p * a.k_st, a.k_st, lds + set * TILE, high + 1 - p, a.hd);
         v_loads.issue(v + (int64_t)p * a.v_st, a.v_st, lds + (2 + set) * TILE, high + 1 - p, a.hd);
     };
+    bool left_out = false;
+    const auto at_edge = [&](int p) { return p < sight.full_from || p + BN - 1 > sight.full_to; };
     const auto take = [&](int p, int set) {
         const unsigned kt = lds + set * TILE, vt = lds + (2 + set) * TILE;
-        const bool edge = p < sight.full_from || p + BN - 1 > sight.full_to;
+        const bool edge = at_edge(p);
         f32x16 x[NB];
-        product<D, NB>(x, q, kt + plain);
-        const auto sees_row = [&](int r) { return sees(mine, p + r); };
+        product<D, NB, 2>(x, [&](int kk) { return q[kk]; }, kt + plain);
         if (edge) {
             asm volatile("");   // a branch, not selects
 #pragma unroll
             for (int u = 0; u < NB; ++u)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[u][i] = sees_row(32 * u + value_row(i)) ? x[u][i] : -INFINITY;
+                for (int i = 0; i < 16; ++i) x[u][i] = sees(mine, p + 32 * u + value_row(i)) ? x[u][i] : -INFINITY;
         }
         float top = x[0][0];
 #pragma unroll
@@ -111,7 +112,9 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_kerne
                 x[u][i] = __builtin_amdgcn_exp2f(fmaf(x[u][i], a.scale_log2, -m));
                 l += x[u][i];
             }
-        add_turned<D, NB>(o, x, vt + turned, vt, edge, sees_row);
+        bf16x8 w[2 * NB];
+        to_operands<NB>(w, x);
+        left_out |= add_turned<D, NB, D / 32>(o, w, vt + turned, edge);
     };
 
     if (low <= high) issue(low, 0);
@@ -123,6 +126,7 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_kerne
         if (sight.any && p + BN > sight.low && p <= sight.high) take(p, set);
     }
 
+    if (left_out) add_left_out<D, BN, false>(o, v, a.v_st, low, high, mine, a.hd, at_edge);
     if (row >= a.T) return;
     const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
     l = __uint_as_float(both[0]) + __uint_as_float(both[1]);

@@ -85,21 +85,24 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dq_ke
         k_loads.issue(k + (int64_t)p * a.k_st, a.k_st, lds + set * TILE, high + 1 - p, a.hd);
         v_loads.issue(v + (int64_t)p * a.v_st, a.v_st, lds + (2 + set) * TILE, high + 1 - p, a.hd);
     };
+    bool left_out = false;
+    const auto at_edge = [&](int p) { return p < sight.full_from || p + 31 > sight.full_to; };
     const auto take = [&](int p, unsigned kt, unsigned vt) {
-        const bool edge = p < sight.full_from || p + 31 > sight.full_to;
+        const bool edge = at_edge(p);
         f32x16 x[1], y[1];
-        product<D, 1>(x, q, kt + plain);
-        product<D, 1>(y, d_o, vt + plain);
-        const auto sees_row = [&](int r) { return sees(mine, p + r); };
+        product<D, 1, 2>(x, [&](int kk) { return q[kk]; }, kt + plain);
+        product<D, 1, 2>(y, [&](int kk) { return d_o[kk]; }, vt + plain);
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             x[0][i] = __builtin_amdgcn_exp2f(fmaf(x[0][i], a.scale_log2, -lse)) * (y[0][i] - delta);
         if (edge) {
             asm volatile("");   // a branch, not selects
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[0][i] = sees_row(value_row(i)) ? x[0][i] : 0.0f;
+            for (int i = 0; i < 16; ++i) x[0][i] = sees(mine, p + value_row(i)) ? x[0][i] : 0.0f;
         }
-        add_turned<D, 1>(dq, x, kt + turned, kt, edge, sees_row);
+        bf16x8 w[2];
+        to_operands<1>(w, x);
+        left_out |= add_turned<D, 1, D / 32>(dq, w, kt + turned, edge);
     };
 
     if (low <= high) issue(low, 0);
@@ -113,6 +116,8 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dq_ke
                 take(p + u, lds + set * TILE + u * R::BYTES, lds + (2 + set) * TILE + u * R::BYTES);
     }
 
+    // a logit of -infinity has a ds of 0, and 0 times an infinity is NaN
+    if (left_out) add_left_out<D, 32, true>(dq, k, a.k_st, low, high, mine, a.hd, at_edge);
     if (row >= a.T) return;
     if (!there) {
 #pragma unroll
@@ -124,10 +129,13 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dq_ke
 }
 
 template <int D, bool PADDED>
-__global__ __launch_bounds__(kWaves * 64, D <= 96 ? 2 : 1) void attention_dkv_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dkv_kernel(AttentionArgs a) {
     using R = Rows<D>;
-    constexpr int BN = D <= 128 ? 64 : 32, TILE = BN * R::BYTES;
-    __shared__ __attribute__((aligned(1024))) unsigned char tiles[4 * TILE];   // q, q, do, do
+    // Heads of 128 and more: the accumulators, k and v leave no registers for two waves a SIMD (heads above 128: for one), so v's rows
+    // stay in LDS.
+    constexpr bool V_IN_LDS = D >= 128;
+    constexpr int BN = V_IN_LDS ? 32 : 64, TILE = BN * R::BYTES;
+    __shared__ __attribute__((aligned(1024))) unsigned char tiles[4 * TILE + (V_IN_LDS ? kRows * R::BYTES : 0)];   // q, q, do, do, v
     __shared__ __attribute__((aligned(16))) float stats[2][2][BN];             // set; lse log2(e), D; token
     __shared__ SpanMemory<kRows> spans;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -138,11 +146,12 @@ __global__ __launch_bounds__(kWaves * 64, D <= 96 ? 2 : 1) void attention_dkv_ke
     const int row0 = (int)(order - unit * (uint32_t)a.tiles) * kRows;   // causal: the first keys are seen by most
     const int row = row0 + wave * 32 + (lane & 31), row_in = min(row, a.T - 1);
 
-    bf16x8 k[D / 16], v[D / 16];
+    bf16x8 k[D / 16], v[V_IN_LDS ? 1 : D / 16];
     load_rows<D>(k, a.k + batch * a.k_sb + kvh * a.k_sh + (int64_t)row_in * a.k_st, row < a.T, a.hd);
-    load_rows<D>(v, a.v + batch * a.v_sb + kvh * a.v_sh + (int64_t)row_in * a.v_st, row < a.T, a.hd);
+    const char* v_head = a.v + batch * a.v_sb + kvh * a.v_sh;
+    if constexpr (!V_IN_LDS) load_rows<D>(v, v_head + (int64_t)row_in * a.v_st, row < a.T, a.hd);
     if constexpr (PADDED) {   // the chunks behind hd are never loaded
-        for (int i = tid; i < 4 * TILE / 16; i += kWaves * 64) reinterpret_cast<u32x4*>(tiles)[i] = u32x4{0, 0, 0, 0};
+        for (int i = tid; i < (int)sizeof(tiles) / 16; i += kWaves * 64) reinterpret_cast<u32x4*>(tiles)[i] = u32x4{0, 0, 0, 0};
     }
     const Span real = find_spans<kRows>(spans, a, batch, row0);
     Span mine = spans.of[wave * 32 + (lane & 31)];   // the tokens that see this lane's key
@@ -182,37 +191,54 @@ __global__ __launch_bounds__(kWaves * 64, D <= 96 ? 2 : 1) void attention_dkv_ke
     const auto keep = [&](int set, float s) {
         if (tid < 2 * BN) stats[set][tid / BN][tid & (BN - 1)] = s;
     };
+    bool left_out = false;
+    const auto at_edge = [&](int p) { return p < sight.full_from || p + 31 > sight.full_to; };
     const auto take = [&](int p, unsigned qt, unsigned dt, const float* lse, const float* delta) {
-        const bool edge = p < sight.full_from || p + 31 > sight.full_to;
+        const bool edge = at_edge(p);
         f32x16 x[1], y[1];
-        product<D, 1>(x, k, qt + plain);
-        product<D, 1>(y, v, dt + plain);
-        const auto sees_row = [&](int r) { return sees(mine, p + r); };
-        const int h = lane >> 5;
+        constexpr int C = D / 32 % 2 == 0 && D >= 128 ? 2 : D / 32, J = D >= 128 ? 1 : 2;
+        bf16x8 w[2], dw[2];
+        {
+            const int h = lane >> 5;
+            product<D, 1, J>(
+                y, [&](int kk) { return V_IN_LDS ? R::plain(lds + 4 * TILE + wave * 32 * R::BYTES + plain, 0, kk) : v[V_IN_LDS ? 0 : kk]; },
+                dt + plain);
+            product<D, 1, J>(x, [&](int kk) { return k[kk]; }, qt + plain);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const f32x4 l = *reinterpret_cast<const f32x4*>(lse + 8 * j + 4 * h), d = *reinterpret_cast<const f32x4*>(delta + 8 * j + 4 * h);
+            for (int j = 0; j < 4; ++j) {
+                const f32x4 l = *reinterpret_cast<const f32x4*>(lse + 8 * j + 4 * h);
+                const f32x4 d = *reinterpret_cast<const f32x4*>(delta + 8 * j + 4 * h);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[0][4 * j + i] = __builtin_amdgcn_exp2f(fmaf(x[0][4 * j + i], a.scale_log2, -l[i]));
-                y[0][4 * j + i] = x[0][4 * j + i] * (y[0][4 * j + i] - d[i]);
+                for (int i = 0; i < 4; ++i) {
+                    x[0][4 * j + i] = __builtin_amdgcn_exp2f(fmaf(x[0][4 * j + i], a.scale_log2, -l[i]));
+                    y[0][4 * j + i] = x[0][4 * j + i] * (y[0][4 * j + i] - d[i]);
+                }
             }
-        }
-        if (edge) {
-            asm volatile("");   // a branch, not selects
+            if (edge) {
+                asm volatile("");   // a branch, not selects
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const bool see = sees_row(value_row(i));
-                x[0][i] = see ? x[0][i] : 0.0f;
-                y[0][i] = see ? y[0][i] : 0.0f;
+                for (int i = 0; i < 16; ++i) {
+                    const bool see = sees(mine, p + value_row(i));
+                    x[0][i] = see ? x[0][i] : 0.0f;
+                    y[0][i] = see ? y[0][i] : 0.0f;
+                }
             }
+            to_operands<1>(w, x);
+            to_operands<1>(dw, y);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        add_turned<D, 1>(dv, x, dt + turned, dt, edge, sees_row);
-        add_turned<D, 1>(dk, y, qt + turned, qt, edge, sees_row);
+        left_out |= add_turned<D, 1, C>(dv, w, dt + turned, edge);
+        // where a token's q is not finite neither is its lse, so that ds is NaN for every key that it sees
+        add_turned<D, 1, C>(dk, dw, qt + turned, edge);
     };
 
     int set = 0;
     if (low <= high) {
+        if constexpr (V_IN_LDS) {   // rows behind the last token repeat it
+            TileLoads<D, kRows, kWaves, PADDED> v_loads;
+            v_loads.init(a.v_st);
+            v_loads.issue(v_head + (int64_t)row0 * a.v_st, a.v_st, lds + 4 * TILE, min(kRows, a.T - row0), a.hd);
+        }
         const float s = issue(0, low, 0);
         keep(0, s);
         int g = 0, p = low;
@@ -236,6 +262,10 @@ __global__ __launch_bounds__(kWaves * 64, D <= 96 ? 2 : 1) void attention_dkv_ke
         }
     }
 
+    if (left_out)
+        for (int g = 0; g < a.group; ++g)
+            add_left_out<D, 32, false>(dv, a.d_o + (int64_t)batch * a.T * a.o_st + (int64_t)(kvh * a.group + g) * a.hd * 2, a.o_st, low, high,
+                                       mine, a.hd, at_edge);
     if (row >= a.T) return;
     if (!there) {
 #pragma unroll
