@@ -172,21 +172,18 @@ __device__ __forceinline__ const char* uniform(const char* p) {
 }
 
 // Direct-to-LDS loads of a tile of BN rows of one tensor, by NW waves. A lane's 16 bytes of
-// instruction i land in LDS chunk (wave N + i) 64 + lane, so the source chunk is the one that
-// belongs there.
+// instruction n land in LDS chunk 64 n + lane, so the source chunk is the one that belongs there.
 template <int D, int BN, int NW, bool PADDED>
 struct TileLoads {
     using R = Rows<D>;
-    static constexpr int N = BN * R::CPR / 64 / NW;
-    static_assert(N * 64 * NW == BN * R::CPR, "whole instructions");
+    static constexpr int TOTAL = BN * R::CPR / 64, N = (TOTAL + NW - 1) / NW;
+    static_assert(TOTAL * 64 == BN * R::CPR, "whole instructions");
     uint32_t offset[N];
-    __device__ __forceinline__ int row_of(int i) const {
-        return (((int)threadIdx.x >> 6) * N + i) * 64 / R::CPR + (((((int)threadIdx.x >> 6) * N + i) * 64) % R::CPR + ((int)threadIdx.x & 63)) / R::CPR;
-    }
+    __device__ __forceinline__ int place_of(int i) const { return (i * NW + ((int)threadIdx.x >> 6)) * 64 + ((int)threadIdx.x & 63); }
+    __device__ __forceinline__ int row_of(int i) const { return place_of(i) / R::CPR; }
     __device__ __forceinline__ int chunk_of(int i) const {
-        const int at = (((int)threadIdx.x >> 6) * N + i) * 64 + ((int)threadIdx.x & 63);
-        const int row = at / R::CPR, slot = at % R::CPR;
-        return slot / R::G * R::G + ((slot % R::G) ^ R::swizzle(row));
+        const int slot = place_of(i) % R::CPR;
+        return slot / R::G * R::G + ((slot % R::G) ^ R::swizzle(row_of(i)));
     }
     __device__ __forceinline__ void init(uint32_t stride) {
 #pragma unroll
@@ -198,8 +195,9 @@ struct TileLoads {
         const char* src = uniform(from);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
+            if (TOTAL % NW != 0 && i * NW + wave >= TOTAL) break;
             const uint32_t at = count >= BN ? offset[i] : (uint32_t)min(row_of(i), count - 1) * stride + (uint32_t)chunk_of(i) * 16;
-            const unsigned dst = tile + (unsigned)(wave * N + i) * 1024;
+            const unsigned dst = tile + (unsigned)(i * NW + wave) * 1024;
             // The wait states: a VMEM instruction that reads an SGPR which VALU wrote needs 5, a
             // direct-to-LDS load after a write of M0 1. Inline, so that the compiler does not wait
             // for the loads of the next tile before it reads this one.

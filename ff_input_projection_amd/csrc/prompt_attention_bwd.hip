@@ -128,17 +128,23 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dq_ke
     store_turned<D>(a.dq + (((int64_t)batch * a.H + head) * a.T + row) * a.hd, true, dq, a.scale, a.hd);
 }
 
+// Workgroups of two halves (heads up to 128): both have the same 128 keys, and each takes every other 32
+// tokens of a tile. So a workgroup takes half as long and there are two waves a SIMD from one workgroup: with a
+// causal mask workgroups differ by their number of tokens, and those that start last (the lightest) fill the gaps.
+constexpr int dkv_halves(int d) { return d <= 128 ? 2 : 1; }
+
 template <int D, bool PADDED>
-__global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dkv_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(kWaves * 64 * dkv_halves(D), 1) void attention_dkv_kernel(AttentionArgs a) {
     using R = Rows<D>;
     // Heads of 128 and more: the accumulators, k and v leave no registers for two waves a SIMD (heads above 128: for one), so v's rows
     // stay in LDS.
     constexpr bool V_IN_LDS = D >= 128;
-    constexpr int BN = V_IN_LDS ? 32 : 64, TILE = BN * R::BYTES;
+    constexpr int H = dkv_halves(D), NW = kWaves * H, BN = 32 * H, TILE = BN * R::BYTES;
     __shared__ __attribute__((aligned(1024))) unsigned char tiles[4 * TILE + (V_IN_LDS ? kRows * R::BYTES : 0)];   // q, q, do, do, v
     __shared__ __attribute__((aligned(16))) float stats[2][2][BN];             // set; lse log2(e), D; token
     __shared__ SpanMemory<kRows> spans;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int tid = threadIdx.x, lane = tid & 63, wave8 = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = wave8 & (kWaves - 1), half = wave8 / kWaves;
     const unsigned lds = (unsigned)(size_t)(lds_void*)tiles;
     const uint32_t order = in_xcd_order(blockIdx.x, a.blocks);
     const uint32_t unit = fp::fastdiv_u31(order, a.div_tiles);
@@ -151,7 +157,7 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dkv_k
     const char* v_head = a.v + batch * a.v_sb + kvh * a.v_sh;
     if constexpr (!V_IN_LDS) load_rows<D>(v, v_head + (int64_t)row_in * a.v_st, row < a.T, a.hd);
     if constexpr (PADDED) {   // the chunks behind hd are never loaded
-        for (int i = tid; i < (int)sizeof(tiles) / 16; i += kWaves * 64) reinterpret_cast<u32x4*>(tiles)[i] = u32x4{0, 0, 0, 0};
+        for (int i = tid; i < (int)sizeof(tiles) / 16; i += NW * 64) reinterpret_cast<u32x4*>(tiles)[i] = u32x4{0, 0, 0, 0};
     }
     const Span real = find_spans<kRows>(spans, a, batch, row0);
     Span mine = spans.of[wave * 32 + (lane & 31)];   // the tokens that see this lane's key
@@ -172,7 +178,7 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dkv_k
 #pragma unroll
         for (int i = 0; i < 16; ++i) dk[t][i] = dv[t][i] = 0.0f;
 
-    TileLoads<D, BN, kWaves, PADDED> q_loads, do_loads;
+    TileLoads<D, BN, NW, PADDED> q_loads, do_loads;
     q_loads.init(a.q_st);
     do_loads.init(a.o_st);
     const unsigned plain = R::plain_base(), turned = R::turned_base();
@@ -193,6 +199,7 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dkv_k
     };
     bool left_out = false;
     const auto at_edge = [&](int p) { return p < sight.full_from || p + 31 > sight.full_to; };
+    const auto mine_at_edge = [&](int p) { return (p - low) / 32 % H == half && at_edge(p); };
     const auto take = [&](int p, unsigned qt, unsigned dt, const float* lse, const float* delta) {
         const bool edge = at_edge(p);
         f32x16 x[1], y[1];
@@ -235,7 +242,7 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dkv_k
     int set = 0;
     if (low <= high) {
         if constexpr (V_IN_LDS) {   // rows behind the last token repeat it
-            TileLoads<D, kRows, kWaves, PADDED> v_loads;
+            TileLoads<D, kRows, NW, PADDED> v_loads;
             v_loads.init(a.v_st);
             v_loads.issue(v_head + (int64_t)row0 * a.v_st, a.v_st, lds + 4 * TILE, min(kRows, a.T - row0), a.hd);
         }
@@ -252,9 +259,9 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dkv_k
             __syncthreads();   // every wave's loads of this tile have landed, and its reads of the other set are done
             float next = 0.0f;
             if (next_g < a.group) next = issue(next_g, next_p, set ^ 1);
-            for (int u = 0; u < BN; u += 32)
-                if (sight.any && p + u + 32 > sight.low && p + u <= sight.high)
-                    take(p + u, lds + set * TILE + u * R::BYTES, lds + (2 + set) * TILE + u * R::BYTES, &stats[set][0][u], &stats[set][1][u]);
+            const int u = 32 * half;
+            if (sight.any && p + u + 32 > sight.low && p + u <= sight.high)
+                take(p + u, lds + set * TILE + u * R::BYTES, lds + (2 + set) * TILE + u * R::BYTES, &stats[set][0][u], &stats[set][1][u]);
             keep(set ^ 1, next);
             set ^= 1;
             g = next_g;
@@ -265,27 +272,55 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dkv_k
     if (left_out)
         for (int g = 0; g < a.group; ++g)
             add_left_out<D, 32, false>(dv, a.d_o + (int64_t)batch * a.T * a.o_st + (int64_t)(kvh * a.group + g) * a.hd * 2, a.o_st, low, high,
-                                       mine, a.hd, at_edge);
-    if (row >= a.T) return;
-    if (!there) {
+                                       mine, a.hd, mine_at_edge);
+    if constexpr (H == 2) {
+        // the halves' sums: the first half takes dk, the second dv (what a wave leaves is as large as its share of the tiles)
+        f32x4* const shared = reinterpret_cast<f32x4*>(tiles) + wave * D * 8 + lane;
+        const auto leave = [&](const f32x16 (&y)[D / 32]) {
 #pragma unroll
-        for (int t = 0; t < D / 32; ++t)
+            for (int j = 0; j < D / 8; ++j)
+                shared[j * 64] = f32x4{y[j >> 2][4 * (j & 3)], y[j >> 2][4 * (j & 3) + 1], y[j >> 2][4 * (j & 3) + 2], y[j >> 2][4 * (j & 3) + 3]};
+        };
+        const auto add = [&](f32x16 (&y)[D / 32]) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) dk[t][i] = dv[t][i] = 0.0f;
+            for (int j = 0; j < D / 8; ++j) {
+                const f32x4 x = shared[j * 64];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[j >> 2][4 * (j & 3) + i] += x[i];
+            }
+        };
+        __syncthreads();   // the tiles are read
+        if (half == 1) leave(dk);
+        __syncthreads();
+        if (half == 0) add(dk);
+        __syncthreads();
+        if (half == 0) leave(dv);
+        __syncthreads();
+        if (half == 1) add(dv);
     }
+    if (row >= a.T) return;
     const int64_t to = (((int64_t)batch * a.KVH + kvh) * a.T + row) * a.hd;
-    store_turned<D>(a.dk + to, true, dk, a.scale, a.hd);
-    store_turned<D>(a.dv + to, true, dv, 1.0f, a.hd);
+    const auto store = [&](__bf16* out, f32x16 (&y)[D / 32], float by) {
+        if (!there) {
+#pragma unroll
+            for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) y[t][i] = 0.0f;
+        }
+        store_turned<D>(out + to, true, y, by, a.hd);
+    };
+    if (H == 1 || half == 0) store(a.dk, dk, a.scale);
+    if (H == 1 || half == 1) store(a.dv, dv, 1.0f);
 }
 
 template <int D>
 void launch(const prompt_attention_desc& d, const AttentionArgs& dq, const AttentionArgs& dkv, hipStream_t st) {
     if (d.head_dim == D) {
         hipLaunchKernelGGL((attention_dq_kernel<D, false>), dim3(dq.blocks), dim3(kWaves * 64), 0, st, dq);
-        hipLaunchKernelGGL((attention_dkv_kernel<D, false>), dim3(dkv.blocks), dim3(kWaves * 64), 0, st, dkv);
+        hipLaunchKernelGGL((attention_dkv_kernel<D, false>), dim3(dkv.blocks), dim3(kWaves * 64 * dkv_halves(D)), 0, st, dkv);
     } else {
         hipLaunchKernelGGL((attention_dq_kernel<D, true>), dim3(dq.blocks), dim3(kWaves * 64), 0, st, dq);
-        hipLaunchKernelGGL((attention_dkv_kernel<D, true>), dim3(dkv.blocks), dim3(kWaves * 64), 0, st, dkv);
+        hipLaunchKernelGGL((attention_dkv_kernel<D, true>), dim3(dkv.blocks), dim3(kWaves * 64 * dkv_halves(D)), 0, st, dkv);
     }
 }
 
