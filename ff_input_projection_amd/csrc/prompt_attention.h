@@ -60,12 +60,12 @@ __device__ __forceinline__ uint32_t in_xcd_order(uint32_t block, uint32_t blocks
     return xcd * q + (xcd < r ? xcd : r) + (block >> 3);
 }
 
-// Which rows of the other side a token sees: first .. last; none where first is kNone.
+// Which rows of the other side a token sees: first .. last; none where first is kNone (then last is it, too).
 struct Span {
     int32_t first, last;
 };
 constexpr int32_t kNone = 0x7FFFFFFF;
-__device__ __forceinline__ bool sees(Span s, int at) { return at >= s.first && at <= s.last && s.first != kNone; }
+__device__ __forceinline__ bool sees(Span s, int at) { return (uint32_t)(at - s.first) <= (uint32_t)(s.last - s.first); }
 
 // LDS of find_spans.
 template <int BM>
@@ -173,35 +173,40 @@ __device__ __forceinline__ const char* uniform(const char* p) {
 
 // Direct-to-LDS loads of a tile of BN rows of one tensor, by NW waves. A lane's 16 bytes of
 // instruction n land in LDS chunk 64 n + lane, so the source chunk is the one that belongs there.
-template <int D, int BN, int NW, bool PADDED>
+// KEEP: the lanes' offsets stay in registers; else they are made again for every tile.
+template <int D, int BN, int NW, bool PADDED, bool KEEP = true>
 struct TileLoads {
     using R = Rows<D>;
     static constexpr int TOTAL = BN * R::CPR / 64, N = (TOTAL + NW - 1) / NW;
     static_assert(TOTAL * 64 == BN * R::CPR, "whole instructions");
-    uint32_t offset[N];
-    __device__ __forceinline__ int place_of(int i) const { return (i * NW + ((int)threadIdx.x >> 6)) * 64 + ((int)threadIdx.x & 63); }
-    __device__ __forceinline__ int row_of(int i) const { return place_of(i) / R::CPR; }
-    __device__ __forceinline__ int chunk_of(int i) const {
-        const int slot = place_of(i) % R::CPR;
-        return slot / R::G * R::G + ((slot % R::G) ^ R::swizzle(row_of(i)));
+    uint32_t offset[KEEP ? N : 1];
+    static __device__ __forceinline__ int row_of(int i, int tid) { return (i * NW * 64 + tid) / R::CPR; }
+    static __device__ __forceinline__ int chunk_of(int i, int tid) {
+        const int slot = (i * NW * 64 + tid) % R::CPR;
+        return slot / R::G * R::G + ((slot % R::G) ^ R::swizzle(row_of(i, tid)));
     }
     __device__ __forceinline__ void init(uint32_t stride) {
+        if constexpr (KEEP) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) offset[i] = (uint32_t)row_of(i) * stride + (uint32_t)chunk_of(i) * 16;
+            for (int i = 0; i < N; ++i) offset[i] = (uint32_t)row_of(i, threadIdx.x) * stride + (uint32_t)chunk_of(i, threadIdx.x) * 16;
+        }
     }
     // Rows from `from` on (wave-uniform) to LDS address `tile`; rows at or past `count` repeat the last one there is.
     __device__ __forceinline__ void issue(const char* from, uint32_t stride, unsigned tile, int count, int hd) const {
-        const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+        int tid = threadIdx.x;
+        if constexpr (!KEEP) asm volatile("" : "+v"(tid));   // what follows from it is not kept since the last tile
+        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const char* src = uniform(from);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             if (TOTAL % NW != 0 && i * NW + wave >= TOTAL) break;
-            const uint32_t at = count >= BN ? offset[i] : (uint32_t)min(row_of(i), count - 1) * stride + (uint32_t)chunk_of(i) * 16;
+            const int row = count >= BN ? row_of(i, tid) : min(row_of(i, tid), count - 1);
+            const uint32_t at = KEEP && count >= BN ? offset[KEEP ? i : 0] : (uint32_t)row * stride + (uint32_t)chunk_of(i, tid) * 16;
             const unsigned dst = tile + (unsigned)(i * NW + wave) * 1024;
             // The wait states: a VMEM instruction that reads an SGPR which VALU wrote needs 5, a
             // direct-to-LDS load after a write of M0 1. Inline, so that the compiler does not wait
             // for the loads of the next tile before it reads this one.
-            if (!PADDED || chunk_of(i) * 8 < hd)
+            if (!PADDED || chunk_of(i, tid) * 8 < hd)
                 asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(at), "s"(src), "{m0}"(dst) : "memory");
         }
     }
@@ -219,6 +224,18 @@ __device__ __forceinline__ void load_rows(bf16x8 (&to)[D / 16], const char* row,
         u32x4 x = {0, 0, 0, 0};
         if (there && 16 * kk + 8 * h < hd) x = *reinterpret_cast<const u32x4*>(row + 32 * kk + 16 * h);
         to[kk] = __builtin_bit_cast(bf16x8, x);
+    }
+}
+
+// Makes the compiler wait here for operands that it loads. It would wait at their first use, inside the
+// loop over the tiles, in every round, and with it for the tile that is on its way.
+template <int N>
+__device__ __forceinline__ void arrived(bf16x8 (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        u32x4 w = __builtin_bit_cast(u32x4, x[i]);
+        asm volatile("" : "+v"(w));
+        x[i] = __builtin_bit_cast(bf16x8, w);
     }
 }
 

@@ -117,6 +117,7 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_kerne
         left_out |= add_turned<D, NB, D / 32>(o, w, vt + turned, edge);
     };
 
+    arrived(q);
     if (low <= high) issue(low, 0);
     int set = 0;
     for (int p = low; p <= high; p += BN, set ^= 1) {

@@ -105,6 +105,9 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dq_ke
         left_out |= add_turned<D, 1, D / 32>(dq, w, kt + turned, edge);
     };
 
+    arrived(q);
+    arrived(d_o);
+    asm volatile("" : "+v"(lse), "+v"(delta));
     if (low <= high) issue(low, 0);
     int set = 0;
     for (int p = low; p <= high; p += BN, set ^= 1) {
@@ -178,7 +181,7 @@ __global__ __launch_bounds__(kWaves * 64 * dkv_halves(D), 1) void attention_dkv_
 #pragma unroll
         for (int i = 0; i < 16; ++i) dk[t][i] = dv[t][i] = 0.0f;
 
-    TileLoads<D, BN, NW, PADDED> q_loads, do_loads;
+    TileLoads<D, BN, NW, PADDED, D < 128> q_loads, do_loads;
     q_loads.init(a.q_st);
     do_loads.init(a.o_st);
     const unsigned plain = R::plain_base(), turned = R::turned_base();
@@ -239,10 +242,12 @@ __global__ __launch_bounds__(kWaves * 64 * dkv_halves(D), 1) void attention_dkv_
         add_turned<D, 1, C>(dk, dw, qt + turned, edge);
     };
 
+    arrived(k);
+    if constexpr (!V_IN_LDS) arrived(v);
     int set = 0;
     if (low <= high) {
         if constexpr (V_IN_LDS) {   // rows behind the last token repeat it
-            TileLoads<D, kRows, NW, PADDED> v_loads;
+            TileLoads<D, kRows, NW, PADDED, false> v_loads;
             v_loads.init(a.v_st);
             v_loads.issue(v_head + (int64_t)row0 * a.v_st, a.v_st, lds + 4 * TILE, min(kRows, a.T - row0), a.hd);
         }
