@@ -67,64 +67,74 @@ struct Span {
 constexpr int32_t kNone = 0x7FFFFFFF;
 __device__ __forceinline__ bool sees(Span s, int at) { return (uint32_t)(at - s.first) <= (uint32_t)(s.last - s.first); }
 
-// LDS of find_spans.
-template <int BM>
-struct SpanMemory {
-    int32_t start, after;
-    uint32_t bits[BM / 32];
-    Span of[BM];
+// The same value in every lane: `f` over all 64 lanes' x (f associative and commutative).
+template <typename F>
+__device__ __forceinline__ int32_t over_lanes(int32_t x, F f) {
+    x = f(x, __builtin_amdgcn_mov_dpp(x, 0xB1, 0xF, 0xF, true));    // quads: lane ^ 1
+    x = f(x, __builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, true));    // lane ^ 2
+    x = f(x, __builtin_amdgcn_mov_dpp(x, 0x141, 0xF, 0xF, true));   // half rows mirrored
+    x = f(x, __builtin_amdgcn_mov_dpp(x, 0x128, 0xF, 0xF, true));   // rows rotated by 8
+    auto r = __builtin_amdgcn_permlane16_swap((uint32_t)x, (uint32_t)x, false, false);
+    x = f((int32_t)r[0], (int32_t)r[1]);
+    r = __builtin_amdgcn_permlane32_swap((uint32_t)x, (uint32_t)x, false, false);
+    return __builtin_amdgcn_readfirstlane(f((int32_t)r[0], (int32_t)r[1]));
+}
+
+// The sequences of a workgroup's rows row0 .. row0 + BM - 1, and of this lane's row, one of the 32 of
+// its wave from `mine0` on (lane % 32): [first, last] tokens.
+struct Spans {
+    Span mine;            // first kNone: of no sequence
+    Span first, last;     // of the first and the last row of the workgroup that is of one
+    int32_t from, to;     // these rows (from > to: none)
 };
-// The sequences of tokens row0 .. row0 + BM - 1 into m.of, as [start, last token of the sequence]; returns the first and
-// the last of these tokens that belong to any (first > last: none). All threads call it; ends with a barrier.
+// Every wave for itself, without LDS: an offset a lane, 64 at a time.
 template <int BM>
-__device__ __forceinline__ Span find_spans(SpanMemory<BM>& m, const AttentionArgs& a, int batch, int row0) {
-    const int tid = threadIdx.x, row = row0 + tid;
-    Span real;
+__device__ __forceinline__ Spans find_spans(const AttentionArgs& a, int batch, int row0, int mine0) {
+    const int lane = threadIdx.x & 63, mine = mine0 + (lane & 31);
+    Spans s;
     if (a.sequences == 0) {
         int length = a.T;
-        if (a.extents) length = min(max(a.extents[batch], 0), a.T);
-        real = Span{row0, min(row0 + BM, length) - 1};
-        if (tid < BM) m.of[tid] = row < length ? Span{0, length - 1} : Span{kNone, kNone};
-        __syncthreads();
-        return real;
+        if (a.extents) length = __builtin_amdgcn_readfirstlane(min(max(a.extents[batch], 0), a.T));
+        s.from = row0;
+        s.to = min(row0 + BM, length) - 1;
+        s.first = s.last = Span{0, length - 1};
+        s.mine = mine < length ? s.first : Span{kNone, kNone};
+        return s;
     }
-    if (tid == 0) {
-        m.start = 0;
-        m.after = a.T;
+    const auto greatest = [](int32_t x, int32_t y) { return max(x, y); };
+    const auto least = [](int32_t x, int32_t y) { return min(x, y); };
+    const auto either = [](int32_t x, int32_t y) { return x | y; };
+    const int32_t begin = a.extents[0], end = a.extents[a.sequences];
+    int32_t at = lane <= a.sequences ? a.extents[lane] : 0;
+    const int first = __builtin_amdgcn_readfirstlane(min(max(begin, 0), a.T)), behind = __builtin_amdgcn_readfirstlane(min(max(end, 0), a.T));
+    s.from = max(row0, first);
+    s.to = min(row0 + BM, behind) - 1;
+    // the greatest offsets not above, and the least above, of the workgroup's first and last row and
+    // the wave's 32; those between the wave's rows as bits
+    int32_t a0 = 0, a1 = a.T, b0 = 0, b1 = a.T, m0 = 0, m1 = a.T, bits = 0;
+    for (int i = 0; i <= a.sequences; i += 64) {
+        if (i > 0) at = i + lane <= a.sequences ? a.extents[i + lane] : 0;
+        const bool is = i + lane <= a.sequences;
+        at = min(max(at, 0), a.T);
+        const auto below = [&](int32_t& x, int32_t& y, int32_t r) {
+            if (is && at <= r) x = max(x, at);
+            if (is && at > r) y = min(y, at);
+        };
+        below(a0, a1, s.from);
+        below(b0, b1, s.to);
+        if (is && at <= mine0) m0 = max(m0, at);
+        if (is && at >= mine0 + 32) m1 = min(m1, at);
+        if (is && at > mine0 && at < mine0 + 32) bits |= (int32_t)(1u << (at - mine0));
     }
-    if (tid < BM / 32) m.bits[tid] = 0;
-    __syncthreads();
-    // the nearest offsets outside the tile, and those inside as bits
-    for (int i = tid; i <= a.sequences; i += blockDim.x) {
-        const int at = min(max(a.extents[i], 0), a.T);
-        if (at <= row0)
-            atomicMax(&m.start, at);
-        else if (at < row0 + BM)
-            atomicOr(&m.bits[(at - row0) >> 5], 1u << ((at - row0) & 31));
-        else
-            atomicMin(&m.after, at);
-    }
-    const int first = min(max(a.extents[0], 0), a.T), behind = min(max(a.extents[a.sequences], 0), a.T);
-    real = Span{max(row0, first), min(row0 + BM, behind) - 1};
-    __syncthreads();
-    if (tid < BM) {
-        int start = m.start, end = m.after;
-#pragma unroll
-        for (int w = 0; w < BM / 32; ++w) {
-            const uint32_t at_or_below = w < (tid >> 5) ? ~0u : w == (tid >> 5) ? ~0u >> (31 - (tid & 31)) : 0u;
-            const uint32_t below = m.bits[w] & at_or_below;
-            if (below) start = row0 + w * 32 + 31 - __clz(below);
-        }
-#pragma unroll
-        for (int w = BM / 32 - 1; w >= 0; --w) {
-            const uint32_t above = w > (tid >> 5) ? ~0u : w == (tid >> 5) ? ~(~0u >> (31 - (tid & 31))) : 0u;
-            const uint32_t later = m.bits[w] & above;
-            if (later) end = row0 + w * 32 + __ffs(later) - 1;
-        }
-        m.of[tid] = row >= first && row < behind ? Span{start, end - 1} : Span{kNone, kNone};
-    }
-    __syncthreads();
-    return real;
+    s.first = Span{over_lanes(a0, greatest), over_lanes(a1, least) - 1};
+    s.last = Span{over_lanes(b0, greatest), over_lanes(b1, least) - 1};
+    m0 = over_lanes(m0, greatest);
+    m1 = over_lanes(m1, least);
+    const uint32_t cuts = (uint32_t)over_lanes(bits, either);
+    const uint32_t below = cuts & (~0u >> (31 - (lane & 31))), above = cuts & ~(~0u >> (31 - (lane & 31)));
+    s.mine = Span{below ? mine0 + 31 - __clz(below) : m0, (above ? mine0 + __ffs(above) - 1 : m1) - 1};
+    if (mine < first || mine >= behind) s.mine = Span{kNone, kNone};
+    return s;
 }
 
 // LDS rows of D elements in chunks of 16 bytes, the chunk index xored with f(row) inside groups of G

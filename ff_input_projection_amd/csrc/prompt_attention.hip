@@ -37,7 +37,6 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_kerne
     using R = Rows<D>;
     constexpr int BN = D <= 128 ? 64 : 32, NB = BN / 32, TILE = BN * R::BYTES;
     __shared__ __attribute__((aligned(1024))) unsigned char tiles[4 * TILE];   // k, k, v, v
-    __shared__ SpanMemory<kRows> spans;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const unsigned lds = (unsigned)(size_t)(lds_void*)tiles;
     const Place at = place_of(a);
@@ -48,15 +47,13 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_kerne
     if constexpr (PADDED) {   // the chunks behind hd are never loaded
         for (int i = tid; i < 4 * TILE / 16; i += kWaves * 64) reinterpret_cast<u32x4*>(tiles)[i] = u32x4{0, 0, 0, 0};
     }
-    const Span real = find_spans<kRows>(spans, a, at.batch, row0);
-    Span mine = spans.of[wave * 32 + (lane & 31)];
+    const Spans spans = find_spans<kRows>(a, at.batch, row0, row0 + wave * 32);
+    Span mine = spans.mine;
     int low = 0, high = -1;
-    if (real.first <= real.last) {
-        low = spans.of[real.first - row0].first;
-        high = a.causal ? real.last : spans.of[real.last - row0].last;
+    if (spans.from <= spans.to) {
+        low = spans.first.first;
+        high = a.causal ? spans.to : spans.last.last;
     }
-    low = __builtin_amdgcn_readfirstlane(low);
-    high = __builtin_amdgcn_readfirstlane(high);
     const bool there = mine.first != kNone;
     if (a.causal && there) mine.last = row;
     const WaveSight sight = wave_sight(mine);
@@ -117,6 +114,7 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_kerne
         left_out |= add_turned<D, NB, D / 32>(o, w, vt + turned, edge);
     };
 
+    if constexpr (PADDED) __syncthreads();
     arrived(q);
     if (low <= high) issue(low, 0);
     int set = 0;

@@ -15,13 +15,13 @@ using namespace fp::dev;
 using fp::AttentionArgs;
 
 constexpr int kWaves = 4, kRows = 32 * kWaves;
+constexpr int64_t kFewBlocks = 192, kManyBlocks = 512;
 
 template <int D, bool PADDED>
 __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dq_kernel(AttentionArgs a) {
     using R = Rows<D>;
     constexpr int BN = D <= 128 ? 64 : 32, TILE = BN * R::BYTES;
     __shared__ __attribute__((aligned(1024))) unsigned char tiles[4 * TILE];   // k, k, v, v
-    __shared__ SpanMemory<kRows> spans;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const unsigned lds = (unsigned)(size_t)(lds_void*)tiles;
     const uint32_t order = in_xcd_order(blockIdx.x, a.blocks);
@@ -51,15 +51,13 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dq_ke
     if constexpr (PADDED) {   // the chunks behind hd are never loaded
         for (int i = tid; i < 4 * TILE / 16; i += kWaves * 64) reinterpret_cast<u32x4*>(tiles)[i] = u32x4{0, 0, 0, 0};
     }
-    const Span real = find_spans<kRows>(spans, a, batch, row0);
-    Span mine = spans.of[wave * 32 + (lane & 31)];
+    const Spans spans = find_spans<kRows>(a, batch, row0, row0 + wave * 32);
+    Span mine = spans.mine;
     int low = 0, high = -1;
-    if (real.first <= real.last) {
-        low = spans.of[real.first - row0].first;
-        high = a.causal ? real.last : spans.of[real.last - row0].last;
+    if (spans.from <= spans.to) {
+        low = spans.first.first;
+        high = a.causal ? spans.to : spans.last.last;
     }
-    low = __builtin_amdgcn_readfirstlane(low);
-    high = __builtin_amdgcn_readfirstlane(high);
     const bool there = mine.first != kNone;
     if (a.causal && there) mine.last = row;
     const WaveSight sight = wave_sight(mine);
@@ -105,6 +103,7 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dq_ke
         left_out |= add_turned<D, 1, D / 32>(dq, w, kt + turned, edge);
     };
 
+    if constexpr (PADDED) __syncthreads();
     arrived(q);
     arrived(d_o);
     asm volatile("" : "+v"(lse), "+v"(delta));
@@ -131,28 +130,24 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dq_ke
     store_turned<D>(a.dq + (((int64_t)batch * a.H + head) * a.T + row) * a.hd, true, dq, a.scale, a.hd);
 }
 
-// Workgroups of two halves (heads up to 128): both have the same 128 keys, and each takes every other 32
-// tokens of a tile. So a workgroup takes half as long and there are two waves a SIMD from one workgroup: with a
-// causal mask workgroups differ by their number of tokens, and those that start last (the lightest) fill the gaps.
-constexpr int dkv_halves(int d) { return d <= 128 ? 2 : 1; }
-
-template <int D, bool PADDED>
-__global__ __launch_bounds__(kWaves * 64 * dkv_halves(D), 1) void attention_dkv_kernel(AttentionArgs a) {
+// Shapes of a workgroup: R rows of waves with 32 keys each, and H waves a row that share these keys and
+// take 32 tokens in turn of each tile of 32 H; their sums are added at the end.
+template <int D, bool PADDED, int RW, int H>
+__global__ __launch_bounds__(64 * RW * H, 1) void attention_dkv_kernel(AttentionArgs a) {
     using R = Rows<D>;
     // Heads of 128 and more: the accumulators, k and v leave no registers for two waves a SIMD (heads above 128: for one), so v's rows
     // stay in LDS.
     constexpr bool V_IN_LDS = D >= 128;
-    constexpr int H = dkv_halves(D), NW = kWaves * H, BN = 32 * H, TILE = BN * R::BYTES;
-    __shared__ __attribute__((aligned(1024))) unsigned char tiles[4 * TILE + (V_IN_LDS ? kRows * R::BYTES : 0)];   // q, q, do, do, v
+    constexpr int NW = RW * H, BM = 32 * RW, BN = 32 * H, TILE = BN * R::BYTES;
+    __shared__ __attribute__((aligned(1024))) unsigned char tiles[4 * TILE + (V_IN_LDS ? BM * R::BYTES : 0)];   // q, q, do, do, v
     __shared__ __attribute__((aligned(16))) float stats[2][2][BN];             // set; lse log2(e), D; token
-    __shared__ SpanMemory<kRows> spans;
-    const int tid = threadIdx.x, lane = tid & 63, wave8 = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wave = wave8 & (kWaves - 1), half = wave8 / kWaves;
+    const int tid = threadIdx.x, lane = tid & 63, place = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = place % RW, turn = place / RW;
     const unsigned lds = (unsigned)(size_t)(lds_void*)tiles;
     const uint32_t order = in_xcd_order(blockIdx.x, a.blocks);
     const uint32_t unit = fp::fastdiv_u31(order, a.div_tiles);
     const int batch = (int)fp::fastdiv_u31(unit, a.div_kvh), kvh = (int)unit - batch * a.KVH;
-    const int row0 = (int)(order - unit * (uint32_t)a.tiles) * kRows;   // causal: the first keys are seen by most
+    const int row0 = (int)(order - unit * (uint32_t)a.tiles) * BM;   // causal: the first keys are seen by most
     const int row = row0 + wave * 32 + (lane & 31), row_in = min(row, a.T - 1);
 
     bf16x8 k[D / 16], v[V_IN_LDS ? 1 : D / 16];
@@ -162,15 +157,13 @@ __global__ __launch_bounds__(kWaves * 64 * dkv_halves(D), 1) void attention_dkv_
     if constexpr (PADDED) {   // the chunks behind hd are never loaded
         for (int i = tid; i < (int)sizeof(tiles) / 16; i += NW * 64) reinterpret_cast<u32x4*>(tiles)[i] = u32x4{0, 0, 0, 0};
     }
-    const Span real = find_spans<kRows>(spans, a, batch, row0);
-    Span mine = spans.of[wave * 32 + (lane & 31)];   // the tokens that see this lane's key
+    const Spans spans = find_spans<BM>(a, batch, row0, row0 + wave * 32);
+    Span mine = spans.mine;   // the tokens that see this lane's key
     int low = 0, high = -1;
-    if (real.first <= real.last) {
-        low = a.causal ? real.first : spans.of[real.first - row0].first;
-        high = spans.of[real.last - row0].last;
+    if (spans.from <= spans.to) {
+        low = a.causal ? spans.from : spans.first.first;
+        high = spans.last.last;
     }
-    low = __builtin_amdgcn_readfirstlane(low);
-    high = __builtin_amdgcn_readfirstlane(high);
     const bool there = mine.first != kNone;
     if (a.causal && there) mine.first = row;
     const WaveSight sight = wave_sight(mine);
@@ -202,7 +195,7 @@ __global__ __launch_bounds__(kWaves * 64 * dkv_halves(D), 1) void attention_dkv_
     };
     bool left_out = false;
     const auto at_edge = [&](int p) { return p < sight.full_from || p + 31 > sight.full_to; };
-    const auto mine_at_edge = [&](int p) { return (p - low) / 32 % H == half && at_edge(p); };
+    const auto mine_at_edge = [&](int p) { return (p - low) / 32 % H == turn && at_edge(p); };
     const auto take = [&](int p, unsigned qt, unsigned dt, const float* lse, const float* delta) {
         const bool edge = at_edge(p);
         f32x16 x[1], y[1];
@@ -242,14 +235,15 @@ __global__ __launch_bounds__(kWaves * 64 * dkv_halves(D), 1) void attention_dkv_
         add_turned<D, 1, C>(dk, dw, qt + turned, edge);
     };
 
+    if constexpr (PADDED) __syncthreads();
     arrived(k);
     if constexpr (!V_IN_LDS) arrived(v);
     int set = 0;
     if (low <= high) {
         if constexpr (V_IN_LDS) {   // rows behind the last token repeat it
-            TileLoads<D, kRows, NW, PADDED, false> v_loads;
+            TileLoads<D, BM, NW, PADDED, false> v_loads;
             v_loads.init(a.v_st);
-            v_loads.issue(v_head + (int64_t)row0 * a.v_st, a.v_st, lds + 4 * TILE, min(kRows, a.T - row0), a.hd);
+            v_loads.issue(v_head + (int64_t)row0 * a.v_st, a.v_st, lds + 4 * TILE, min(BM, a.T - row0), a.hd);
         }
         const float s = issue(0, low, 0);
         keep(0, s);
@@ -264,7 +258,7 @@ __global__ __launch_bounds__(kWaves * 64 * dkv_halves(D), 1) void attention_dkv_
             __syncthreads();   // every wave's loads of this tile have landed, and its reads of the other set are done
             float next = 0.0f;
             if (next_g < a.group) next = issue(next_g, next_p, set ^ 1);
-            const int u = 32 * half;
+            const int u = 32 * turn;
             if (sight.any && p + u + 32 > sight.low && p + u <= sight.high)
                 take(p + u, lds + set * TILE + u * R::BYTES, lds + (2 + set) * TILE + u * R::BYTES, &stats[set][0][u], &stats[set][1][u]);
             keep(set ^ 1, next);
@@ -278,30 +272,33 @@ __global__ __launch_bounds__(kWaves * 64 * dkv_halves(D), 1) void attention_dkv_
         for (int g = 0; g < a.group; ++g)
             add_left_out<D, 32, false>(dv, a.d_o + (int64_t)batch * a.T * a.o_st + (int64_t)(kvh * a.group + g) * a.hd * 2, a.o_st, low, high,
                                        mine, a.hd, mine_at_edge);
-    if constexpr (H == 2) {
-        // the halves' sums: the first half takes dk, the second dv (what a wave leaves is as large as its share of the tiles)
+    if constexpr (H > 1) {
+        // a row's sums: its first wave takes dk, its second dv, from what the others leave in the tiles' place
         f32x4* const shared = reinterpret_cast<f32x4*>(tiles) + wave * D * 8 + lane;
-        const auto leave = [&](const f32x16 (&y)[D / 32]) {
+        constexpr int NEXT = RW * D * 8;   // the next wave of the row
+        const auto sum_up = [&](f32x16 (&y)[D / 32], int taker) {
+            __syncthreads();   // the tiles, or the last sums, are read
+            if (turn != taker) {
+                f32x4* const to = shared + (turn > taker ? turn - 1 : turn) * NEXT;
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j)
-                shared[j * 64] = f32x4{y[j >> 2][4 * (j & 3)], y[j >> 2][4 * (j & 3) + 1], y[j >> 2][4 * (j & 3) + 2], y[j >> 2][4 * (j & 3) + 3]};
-        };
-        const auto add = [&](f32x16 (&y)[D / 32]) {
+                for (int j = 0; j < D / 8; ++j)
+                    to[j * 64] = f32x4{y[j >> 2][4 * (j & 3)], y[j >> 2][4 * (j & 3) + 1], y[j >> 2][4 * (j & 3) + 2], y[j >> 2][4 * (j & 3) + 3]};
+            }
+            __syncthreads();
+            if (turn == taker) {
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j) {
-                const f32x4 x = shared[j * 64];
+                for (int g = 0; g < H - 1; ++g)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[j >> 2][4 * (j & 3) + i] += x[i];
+                    for (int j = 0; j < D / 8; ++j) {
+                        const f32x4 x = shared[g * NEXT + j * 64];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) y[j >> 2][4 * (j & 3) + i] += x[i];
+                    }
             }
         };
-        __syncthreads();   // the tiles are read
-        if (half == 1) leave(dk);
-        __syncthreads();
-        if (half == 0) add(dk);
-        __syncthreads();
-        if (half == 0) leave(dv);
-        __syncthreads();
-        if (half == 1) add(dv);
+        static_assert((H - 1) * NEXT * 16 <= 4 * TILE, "the sums fit the tiles");
+        sum_up(dk, 0);
+        sum_up(dv, 1);
     }
     if (row >= a.T) return;
     const int64_t to = (((int64_t)batch * a.KVH + kvh) * a.T + row) * a.hd;
@@ -314,19 +311,40 @@ __global__ __launch_bounds__(kWaves * 64 * dkv_halves(D), 1) void attention_dkv_
         }
         store_turned<D>(out + to, true, y, by, a.hd);
     };
-    if (H == 1 || half == 0) store(a.dk, dk, a.scale);
-    if (H == 1 || half == 1) store(a.dv, dv, 1.0f);
+    if (H == 1 || turn == 0) store(a.dk, dk, a.scale);
+    if (H == 1 || turn == 1) store(a.dv, dv, 1.0f);
+}
+
+template <int D, int RW, int H>
+void launch_dkv(const prompt_attention_desc& d, AttentionArgs a, hipStream_t st) {
+    a.tiles = (int32_t)((d.tokens + 32 * RW - 1) / (32 * RW));
+    a.div_tiles = fp::make_fastdiv_u31((uint32_t)a.tiles);
+    a.blocks = (uint32_t)(d.batch * a.KVH * a.tiles);
+    if (d.head_dim == D)
+        hipLaunchKernelGGL((attention_dkv_kernel<D, false, RW, H>), dim3(a.blocks), dim3(64 * RW * H), 0, st, a);
+    else
+        hipLaunchKernelGGL((attention_dkv_kernel<D, true, RW, H>), dim3(a.blocks), dim3(64 * RW * H), 0, st, a);
 }
 
 template <int D>
-void launch(const prompt_attention_desc& d, const AttentionArgs& dq, const AttentionArgs& dkv, hipStream_t st) {
-    if (d.head_dim == D) {
-        hipLaunchKernelGGL((attention_dq_kernel<D, false>), dim3(dq.blocks), dim3(kWaves * 64), 0, st, dq);
-        hipLaunchKernelGGL((attention_dkv_kernel<D, false>), dim3(dkv.blocks), dim3(kWaves * 64 * dkv_halves(D)), 0, st, dkv);
-    } else {
-        hipLaunchKernelGGL((attention_dq_kernel<D, true>), dim3(dq.blocks), dim3(kWaves * 64), 0, st, dq);
-        hipLaunchKernelGGL((attention_dkv_kernel<D, true>), dim3(dkv.blocks), dim3(kWaves * 64 * dkv_halves(D)), 0, st, dkv);
-    }
+void launch(const prompt_attention_desc& d, AttentionArgs a, hipStream_t st) {
+    a.tiles = (int32_t)((d.tokens + kRows - 1) / kRows);
+    a.div_tiles = fp::make_fastdiv_u31((uint32_t)a.tiles);
+    a.blocks = (uint32_t)(d.batch * d.n_heads * a.tiles);
+    if (d.head_dim == D)
+        hipLaunchKernelGGL((attention_dq_kernel<D, false>), dim3(a.blocks), dim3(kWaves * 64), 0, st, a);
+    else
+        hipLaunchKernelGGL((attention_dq_kernel<D, true>), dim3(a.blocks), dim3(kWaves * 64), 0, st, a);
+    // workgroups of 128 keys
+    const int64_t blocks = d.batch * a.KVH * ((d.tokens + 127) / 128);
+    if constexpr (D > 128)
+        launch_dkv<D, 4, 1>(d, a, st);
+    else if (blocks < kFewBlocks)
+        launch_dkv<D, 2, 4>(d, a, st);
+    else if (D == 128 || blocks < kManyBlocks)
+        launch_dkv<D, 4, 2>(d, a, st);
+    else
+        launch_dkv<D <= 96 ? D : 96, 4, 1>(d, a, st);
 }
 
 }  // namespace
@@ -334,18 +352,13 @@ void launch(const prompt_attention_desc& d, const AttentionArgs& dq, const Atten
 namespace fp {
 
 hipError_t launch_attention_backward(const prompt_attention_desc& d, const AttentionPlan& p, AttentionArgs a, hipStream_t st) {
-    a.tiles = (int32_t)((d.tokens + kRows - 1) / kRows);
-    a.div_tiles = make_fastdiv_u31((uint32_t)a.tiles);
-    a.blocks = (uint32_t)(d.batch * d.n_heads * a.tiles);
-    AttentionArgs b = a;
-    b.blocks = (uint32_t)(d.batch * a.KVH * a.tiles);
     switch (p.dim) {
-        case 32: launch<32>(d, a, b, st); break;
-        case 64: launch<64>(d, a, b, st); break;
-        case 96: launch<96>(d, a, b, st); break;
-        case 128: launch<128>(d, a, b, st); break;
-        case 192: launch<192>(d, a, b, st); break;
-        default: launch<256>(d, a, b, st);
+        case 32: launch<32>(d, a, st); break;
+        case 64: launch<64>(d, a, st); break;
+        case 96: launch<96>(d, a, st); break;
+        case 128: launch<128>(d, a, st); break;
+        case 192: launch<192>(d, a, st); break;
+        default: launch<256>(d, a, st);
     }
     return hipGetLastError();
 }
