@@ -42,6 +42,18 @@ struct AttentionPlan {
     size_t run_workspace = 0, backward_workspace = 0;
 };
 
+// Whether workgroups of 128 tokens (4 waves, two workgroups a CU) are so few, or with a causal mask so different, that
+// workgroups of 64 with 4 waves a row are faster. Forward pass, heads of 64 and 128, us, workgroups of 128 / of 64:
+//   8 heads x 2048 tokens (128 workgroups)  37 / 20, 52 / 31      the same, causal  37 / 20, 52 / 29
+//   64 x 512 (256)                          13 / 13, 18 / 24      16 x 2048, causal (256)  38 / 29, 52 / 38
+//   128 x 512 (512)                         17 / 22, 30 / 47      16 x 4096, causal (512)  89 / 65, 132 / 121
+//   32 x 2048 (512)                         51 / 59, 83 / 114     64 x 2048, causal (1024) 74 / 75, 122 / 141
+// Up to 128 tokens there are one or two tiles of keys, and nothing to share. Large groups gain less
+// (32 heads on 8 of 128 x 2048, causal, 512: 57 / 71).
+inline bool few_workgroups(int64_t blocks, const prompt_attention_desc& d) {
+    return d.tokens > 128 && (blocks < 256 || (d.tokens >= 1024 && blocks < (d.causal && d.head_dim <= 64 ? 768 : 512)));
+}
+
 hipError_t launch_attention(const prompt_attention_desc& d, const AttentionPlan& p, AttentionArgs a, hipStream_t st);
 hipError_t launch_attention_backward(const prompt_attention_desc& d, const AttentionPlan& p, AttentionArgs a, hipStream_t st);
 
@@ -87,9 +99,10 @@ struct Spans {
     Span first, last;     // of the first and the last row of the workgroup that is of one
     int32_t from, to;     // these rows (from > to: none)
 };
-// Every wave for itself, without LDS: an offset a lane, 64 at a time.
+// Every wave for itself, without LDS: an offset a lane, 64 at a time. starts, ends: which of the two are
+// wanted (reductions over the lanes are what it takes most of its time for).
 template <int BM>
-__device__ __forceinline__ Spans find_spans(const AttentionArgs& a, int batch, int row0, int mine0) {
+__device__ __forceinline__ Spans find_spans(const AttentionArgs& a, int batch, int row0, int mine0, bool starts, bool ends) {
     const int lane = threadIdx.x & 63, mine = mine0 + (lane & 31);
     Spans s;
     if (a.sequences == 0) {
@@ -126,10 +139,18 @@ __device__ __forceinline__ Spans find_spans(const AttentionArgs& a, int batch, i
         if (is && at >= mine0 + 32) m1 = min(m1, at);
         if (is && at > mine0 && at < mine0 + 32) bits |= (int32_t)(1u << (at - mine0));
     }
-    s.first = Span{over_lanes(a0, greatest), over_lanes(a1, least) - 1};
-    s.last = Span{over_lanes(b0, greatest), over_lanes(b1, least) - 1};
-    m0 = over_lanes(m0, greatest);
-    m1 = over_lanes(m1, least);
+    if (starts) {
+        a0 = over_lanes(a0, greatest);
+        b0 = over_lanes(b0, greatest);
+        m0 = over_lanes(m0, greatest);
+    }
+    if (ends) {
+        a1 = over_lanes(a1, least);
+        b1 = over_lanes(b1, least);
+        m1 = over_lanes(m1, least);
+    }
+    s.first = Span{a0, a1 - 1};
+    s.last = Span{b0, b1 - 1};
     const uint32_t cuts = (uint32_t)over_lanes(bits, either);
     const uint32_t below = cuts & (~0u >> (31 - (lane & 31))), above = cuts & ~(~0u >> (31 - (lane & 31)));
     s.mine = Span{below ? mine0 + 31 - __clz(below) : m0, (above ? mine0 + __ffs(above) - 1 : m1) - 1};
@@ -159,9 +180,10 @@ struct Rows {
         return *(const __attribute__((address_space(3))) bf16x8*)(size_t)at;
     }
     // Operand A of Y^T: element 32 t + lane % 32 of rows 16 s + 4 (lane / 32) + {0 .. 3, 8 .. 11}.
-    static __device__ __forceinline__ unsigned turned_base() {
+    // part: of two, where a wave has every other tile of Y^T.
+    static __device__ __forceinline__ unsigned turned_base(int part = 0) {
         const int lane = threadIdx.x & 63, g = lane >> 4, q = lane & 15;
-        const int row = 4 * (g >> 1) + (q >> 2), chunk = (g & 1) * 2 + ((q & 3) >> 1);
+        const int row = 4 * (g >> 1) + (q >> 2), chunk = 4 * part + (g & 1) * 2 + ((q & 3) >> 1);
         return (unsigned)(row * BYTES + ((chunk ^ swizzle(row)) << 4) + (q & 1) * 8);
     }
     static __device__ __forceinline__ i16x4 turned_half(unsigned base, int t, int s, int j) {
@@ -284,9 +306,9 @@ __device__ __forceinline__ void product(f32x16 (&x)[NB], const B& b, unsigned ba
     const auto read = [&](int k) {
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            w[(k / J) & 1][j] = b(k + j);
+            w[k / J % 2][j] = b(k + j);
 #pragma unroll
-            for (int u = 0; u < NB; ++u) a[(k / J) & 1][j][u] = R::plain(base, u, k + j);
+            for (int u = 0; u < NB; ++u) a[k / J % 2][j][u] = R::plain(base, u, k + j);
         }
     };
 #pragma unroll
@@ -301,24 +323,25 @@ __device__ __forceinline__ void product(f32x16 (&x)[NB], const B& b, unsigned ba
         for (int j = 0; j < J; ++j)
 #pragma unroll
             for (int u = 0; u < NB; ++u)
-                x[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[(k / J) & 1][j][u], w[(k / J) & 1][j], x[u], 0, 0, 0);
+                x[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[k / J % 2][j][u], w[k / J % 2][j], x[u], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
     }
 }
 
-// Y^T += A'^T X for the tile of 32 NB rows whose turned base is given; C tiles of Y^T a group.
+// Y^T += A'^T X for the tile of 32 NB rows whose turned base is given; C tiles of Y^T a group. PARTS: the wave has every
+// PARTS-th tile (32 elements of the heads) of Y^T alone, the first as turned_base says.
 // Where the mask hides some of the tile's rows from some of the wave's (`edge`), their values in X
 // are 0, but 0 times an infinity or NaN is NaN. A product of the tile with zeros tells whether it
 // holds any; then they are left out here, and true is returned: add_left_out has to follow.
-template <int D, int NB, int C>
-__device__ __forceinline__ bool add_turned(f32x16 (&y)[D / 32], const bf16x8 (&x)[2 * NB], unsigned base, bool edge) {
+template <int D, int NB, int C, int PARTS = 1>
+__device__ __forceinline__ bool add_turned(f32x16 (&y)[D / 32 / PARTS], const bf16x8 (&x)[2 * NB], unsigned base, bool edge) {
     using R = Rows<D>;
-    constexpr int T = D / 32, S = 2 * NB, P = T / C;   // P groups a step
+    constexpr int T = D / 32 / PARTS, S = 2 * NB, P = T / C;   // P groups a step
     static_assert(P * C == T, "whole groups");
     bf16x8 a[2][C];
     const auto read = [&](int i) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) a[i & 1][c] = R::turned(base, i % P * C + c, i / P);
+        for (int c = 0; c < C; ++c) a[i & 1][c] = R::turned(base, (i % P * C + c) * PARTS, i / P);
     };
     bool all_finite = true;
     if (edge) {
@@ -354,9 +377,9 @@ __device__ __forceinline__ bool add_turned(f32x16 (&y)[D / 32], const bf16x8 (&x
 // What add_turned left out of the tiles of BN rows from `low` on, up to row `high`: their infinities and
 // NaN (as NaN, with AS_NAN), straight from memory, added to the rows that see them. `rows`: row 0; `edge(p)`: whether tile p was
 // one. Behind the loop over the tiles, and not in it, where it would cost every wave registers.
-template <int D, int BN, bool AS_NAN, typename Edge>
-__device__ __forceinline__ void add_left_out(f32x16 (&y)[D / 32], const char* rows, uint32_t stride, int low, int high, Span mine,
-                                             int hd, Edge edge) {
+template <int D, int BN, bool AS_NAN, int PARTS = 1, typename Edge>
+__device__ __forceinline__ void add_left_out(f32x16 (&y)[D / 32 / PARTS], const char* rows, uint32_t stride, int low, int high,
+                                             Span mine, int hd, Edge edge, int part = 0) {
     const int h = (threadIdx.x & 63) >> 5;
 #pragma unroll 1
     for (int p = low; p <= high; p += BN) {
@@ -365,9 +388,10 @@ __device__ __forceinline__ void add_left_out(f32x16 (&y)[D / 32], const char* ro
         for (int row = p; row < p + BN && row <= high; ++row) {
             const bool see = sees(mine, row);
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
+            for (int i = 0; i < D / 8 / PARTS; ++i) {
+                const int d = 32 * ((i >> 2) * PARTS + part) + 8 * (i & 3);
                 u32x2 e = {0, 0};
-                if (8 * i < hd) e = *reinterpret_cast<const u32x2*>(rows + (int64_t)row * stride + 16 * i + 8 * h);
+                if (d < hd) e = *reinterpret_cast<const u32x2*>(rows + (int64_t)row * stride + 2 * d + 8 * h);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t bits = k & 1 ? e[k >> 1] & 0xFFFF0000u : e[k >> 1] << 16;
@@ -378,13 +402,13 @@ __device__ __forceinline__ void add_left_out(f32x16 (&y)[D / 32], const char* ro
     }
 }
 
-// Y^T times `by` (and the lane's row of it) as bf16 to row `to`, elements below hd: a lane and the one
+// Y^T times `by` as bf16, each lane's row of it to its `to`, elements below hd: a lane and the one
 // 32 further exchange halves, so that each stores 16 bytes.
-template <int D>
-__device__ __forceinline__ void store_turned(__bf16* to, bool there, const f32x16 (&y)[D / 32], float by, int hd) {
+template <int D, int PARTS = 1>
+__device__ __forceinline__ void store_turned(__bf16* to, const f32x16 (&y)[D / 32 / PARTS], float by, int hd, int part = 0) {
     const int h = (threadIdx.x & 63) >> 5;
 #pragma unroll
-    for (int t = 0; t < D / 32; ++t)
+    for (int t = 0; t < D / 32 / PARTS; ++t)
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             bf16x4 a, b;
@@ -401,9 +425,35 @@ __device__ __forceinline__ void store_turned(__bf16* to, bool there, const f32x1
                 out[i] = r[0];
                 out[2 + i] = r[1];
             }
-            const int d = 32 * t + 16 * p + 8 * h;
-            if (there && d < hd) *reinterpret_cast<u32x4*>(to + d) = out;
+            const int d = 32 * (t * PARTS + part) + 16 * p + 8 * h;
+            if (d < hd) *reinterpret_cast<u32x4*>(to + d) = out;
         }
+}
+
+// Sums of the H waves of each of RW rows of waves into wave `taker` of the row (turn: which one this is), through `memory`
+// (16-byte aligned LDS of (H - 1) RW 128 D bytes, which other waves may still read).
+template <int D, int RW, int H>
+__device__ __forceinline__ void sum_up(f32x16 (&y)[D / 32], int taker, int wave, int turn, unsigned char* memory) {
+    constexpr int NEXT = RW * D * 8;   // from one wave of a row to its next, in pieces of 16 bytes
+    f32x4* const shared = reinterpret_cast<f32x4*>(memory) + wave * D * 8 + (threadIdx.x & 63);
+    __syncthreads();
+    if (turn != taker) {
+        f32x4* const to = shared + (turn > taker ? turn - 1 : turn) * NEXT;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+            to[j * 64] = f32x4{y[j >> 2][4 * (j & 3)], y[j >> 2][4 * (j & 3) + 1], y[j >> 2][4 * (j & 3) + 2], y[j >> 2][4 * (j & 3) + 3]};
+    }
+    __syncthreads();
+    if (turn == taker) {
+#pragma unroll
+        for (int g = 0; g < H - 1; ++g)
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) {
+                const f32x4 x = shared[g * NEXT + j * 64];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[j >> 2][4 * (j & 3) + i] += x[i];
+            }
+    }
 }
 
 // The first row of a wave's 32 that is of a sequence, the last one, and what all of them, and any of

@@ -17,7 +17,6 @@ namespace {
 using namespace fp::dev;
 using fp::AttentionArgs;
 
-constexpr int kWaves = 4, kRows = 32 * kWaves;
 constexpr float kLowest = -3.0e38f;   // the running maximum before any key
 constexpr float kSlack = 8.0f;        // how far (log2) a logit may pass it before it moves
 
@@ -32,22 +31,26 @@ __device__ __forceinline__ Place place_of(const AttentionArgs& a) {
     return p;
 }
 
-template <int D, bool PADDED>
-__global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_kernel(AttentionArgs a) {
+// Shapes of a workgroup: RW rows of waves with 32 tokens each, and H waves a row that share them and take
+// 32 NB keys in turn of each tile of 32 NB H; what they have is joined at the end.
+template <int D, bool PADDED, int RW, int H, int NB>
+__global__ __launch_bounds__(64 * RW * H, RW * H == 4 && D <= 128 ? 2 : 1) void attention_kernel(AttentionArgs a) {
     using R = Rows<D>;
-    constexpr int BN = D <= 128 ? 64 : 32, NB = BN / 32, TILE = BN * R::BYTES;
+    constexpr int NW = RW * H, BM = 32 * RW, BW = 32 * NB, BN = BW * H, TILE = BN * R::BYTES;
     __shared__ __attribute__((aligned(1024))) unsigned char tiles[4 * TILE];   // k, k, v, v
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int tid = threadIdx.x, lane = tid & 63, place = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = place % RW, turn = H > 1 ? place / RW : 0;
+    __shared__ float maxima[H > 1 ? H : 1][BM], sums[H > 1 ? H : 1][BM];
     const unsigned lds = (unsigned)(size_t)(lds_void*)tiles;
     const Place at = place_of(a);
-    const int row0 = at.tile * kRows, row = row0 + wave * 32 + (lane & 31);
+    const int row0 = at.tile * BM, row = row0 + wave * 32 + (lane & 31);
 
     bf16x8 q[D / 16];
     load_rows<D>(q, a.q + at.batch * a.q_sb + at.head * a.q_sh + (int64_t)min(row, a.T - 1) * a.q_st, row < a.T, a.hd);
     if constexpr (PADDED) {   // the chunks behind hd are never loaded
-        for (int i = tid; i < 4 * TILE / 16; i += kWaves * 64) reinterpret_cast<u32x4*>(tiles)[i] = u32x4{0, 0, 0, 0};
+        for (int i = tid; i < 4 * TILE / 16; i += NW * 64) reinterpret_cast<u32x4*>(tiles)[i] = u32x4{0, 0, 0, 0};
     }
-    const Spans spans = find_spans<kRows>(a, at.batch, row0, row0 + wave * 32);
+    const Spans spans = find_spans<BM>(a, at.batch, row0, row0 + wave * 32, true, !a.causal);
     Span mine = spans.mine;
     int low = 0, high = -1;
     if (spans.from <= spans.to) {
@@ -67,7 +70,7 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_kerne
 
     const char* k = a.k + at.batch * a.k_sb + at.kvh * a.k_sh;
     const char* v = a.v + at.batch * a.v_sb + at.kvh * a.v_sh;
-    TileLoads<D, BN, kWaves, PADDED> k_loads, v_loads;
+    TileLoads<D, BN, NW, PADDED> k_loads, v_loads;
     k_loads.init(a.k_st);
     v_loads.init(a.v_st);
     const unsigned plain = R::plain_base(), turned = R::turned_base();
@@ -76,9 +79,9 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_kerne
         v_loads.issue(v + (int64_t)p * a.v_st, a.v_st, lds + (2 + set) * TILE, high + 1 - p, a.hd);
     };
     bool left_out = false;
-    const auto at_edge = [&](int p) { return p < sight.full_from || p + BN - 1 > sight.full_to; };
-    const auto take = [&](int p, int set) {
-        const unsigned kt = lds + set * TILE, vt = lds + (2 + set) * TILE;
+    const auto at_edge = [&](int p) { return p < sight.full_from || p + BW - 1 > sight.full_to; };
+    const auto mine_at_edge = [&](int p) { return (p - low) / BW % H == turn && at_edge(p); };
+    const auto take = [&](int p, unsigned kt, unsigned vt) {
         const bool edge = at_edge(p);
         f32x16 x[NB];
         product<D, NB, 2>(x, [&](int kk) { return q[kk]; }, kt + plain);
@@ -122,31 +125,69 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_kerne
         wait_loads();
         __syncthreads();   // every wave's loads of this tile have landed, and its reads of the other set are done
         if (p + BN <= high) issue(p + BN, set ^ 1);
-        if (sight.any && p + BN > sight.low && p <= sight.high) take(p, set);
+        const int u = BW * turn;
+        if (sight.any && p + u + BW > sight.low && p + u <= sight.high)
+            take(p + u, lds + set * TILE + u * R::BYTES, lds + (2 + set) * TILE + u * R::BYTES);
     }
 
-    if (left_out) add_left_out<D, BN, false>(o, v, a.v_st, low, high, mine, a.hd, at_edge);
-    if (row >= a.T) return;
     const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
     l = __uint_as_float(both[0]) + __uint_as_float(both[1]);
+    if constexpr (H > 1) {
+        // the row's greatest maximum, and its sum of exponentials
+        if (lane < 32) maxima[turn][wave * 32 + lane] = m;
+        __syncthreads();
+        float to = m;
+#pragma unroll
+        for (int g = 0; g < H; ++g) to = fmaxf(to, maxima[g][wave * 32 + (lane & 31)]);
+        const float down = __builtin_amdgcn_exp2f(m - to);
+        m = to;
+        if (lane < 32) sums[turn][wave * 32 + lane] = l * down;
+#pragma unroll
+        for (int t = 0; t < D / 32; ++t) o[t] *= down;
+    }
+    // behind the last change of the maximum: 0 times an infinity is NaN
+    if (left_out) add_left_out<D, BW, false>(o, v, a.v_st, low, high, mine, a.hd, mine_at_edge);
+    if constexpr (H > 1) {
+        static_assert((H - 1) * RW * 128 * D <= 4 * TILE, "the sums fit the tiles");
+        sum_up<D, RW, H>(o, 0, wave, turn, tiles);
+        l = 0.0f;
+#pragma unroll
+        for (int g = 0; g < H; ++g) l += sums[g][wave * 32 + (lane & 31)];
+    }
+    if (row >= a.T || turn > 0) return;
     if (!there) {
 #pragma unroll
         for (int t = 0; t < D / 32; ++t)
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[t][i] = 0.0f;
     }
-    store_turned<D>(a.o + ((int64_t)at.batch * a.T + row) * ((int64_t)a.H * a.hd) + (int64_t)at.head * a.hd, true, o,
+    store_turned<D>(a.o + ((int64_t)at.batch * a.T + row) * ((int64_t)a.H * a.hd) + (int64_t)at.head * a.hd, o,
                     there ? 1.0f / l : 0.0f, a.hd);
     if (a.lse && lane < 32)
         a.lse[((int64_t)at.batch * a.H + at.head) * a.T + row] = there ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
 }
 
+template <int D, int RW, int H, int NB>
+void launch_shape(const prompt_attention_desc& d, AttentionArgs a, hipStream_t st) {
+    a.tiles = (int32_t)((d.tokens + 32 * RW - 1) / (32 * RW));
+    a.div_tiles = fp::make_fastdiv_u31((uint32_t)a.tiles);
+    a.blocks = (uint32_t)(d.batch * d.n_heads * a.tiles);
+    if (d.head_dim == D)
+        hipLaunchKernelGGL((attention_kernel<D, false, RW, H, NB>), dim3(a.blocks), dim3(64 * RW * H), 0, st, a);
+    else
+        hipLaunchKernelGGL((attention_kernel<D, true, RW, H, NB>), dim3(a.blocks), dim3(64 * RW * H), 0, st, a);
+}
+
 template <int D>
 void launch(const prompt_attention_desc& d, const AttentionArgs& a, hipStream_t st) {
-    if (d.head_dim == D)
-        hipLaunchKernelGGL((attention_kernel<D, false>), dim3(a.blocks), dim3(kWaves * 64), 0, st, a);
+    // workgroups of 128 tokens
+    const int64_t blocks = d.batch * d.n_heads * ((d.tokens + 127) / 128);
+    if constexpr (D > 128)
+        launch_shape<D, 4, 1, 1>(d, a, st);
+    else if (fp::few_workgroups(blocks, d))
+        launch_shape<D, 2, 4, 1>(d, a, st);
     else
-        hipLaunchKernelGGL((attention_kernel<D, true>), dim3(a.blocks), dim3(kWaves * 64), 0, st, a);
+        launch_shape<D, 4, 1, 2>(d, a, st);
 }
 
 }  // namespace
@@ -154,9 +195,6 @@ void launch(const prompt_attention_desc& d, const AttentionArgs& a, hipStream_t 
 namespace fp {
 
 hipError_t launch_attention(const prompt_attention_desc& d, const AttentionPlan& p, AttentionArgs a, hipStream_t st) {
-    a.tiles = (int32_t)((d.tokens + kRows - 1) / kRows);
-    a.blocks = (uint32_t)(d.batch * d.n_heads * a.tiles);
-    a.div_tiles = make_fastdiv_u31((uint32_t)a.tiles);
     switch (p.dim) {
         case 32: launch<32>(d, a, st); break;
         case 64: launch<64>(d, a, st); break;

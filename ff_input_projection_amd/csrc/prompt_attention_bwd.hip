@@ -14,21 +14,22 @@ namespace {
 using namespace fp::dev;
 using fp::AttentionArgs;
 
-constexpr int kWaves = 4, kRows = 32 * kWaves;
-constexpr int64_t kFewBlocks = 192, kManyBlocks = 512;
 
-template <int D, bool PADDED>
-__global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dq_kernel(AttentionArgs a) {
+// Shapes of a workgroup: RW rows of waves with 32 tokens each, and H waves a row that share them and take S
+// times 32 keys in turn of each tile of 32 H S; their sums are added at the end.
+template <int D, bool PADDED, int RW, int H, int S>
+__global__ __launch_bounds__(64 * RW * H, RW * H == 4 && D <= 128 ? 2 : 1) void attention_dq_kernel(AttentionArgs a) {
     using R = Rows<D>;
-    constexpr int BN = D <= 128 ? 64 : 32, TILE = BN * R::BYTES;
+    constexpr int NW = RW * H, BM = 32 * RW, BN = 32 * H * S, TILE = BN * R::BYTES;
     __shared__ __attribute__((aligned(1024))) unsigned char tiles[4 * TILE];   // k, k, v, v
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int tid = threadIdx.x, lane = tid & 63, place = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = place % RW, turn = H > 1 ? place / RW : 0;
     const unsigned lds = (unsigned)(size_t)(lds_void*)tiles;
     const uint32_t order = in_xcd_order(blockIdx.x, a.blocks);
     const uint32_t rest = fp::fastdiv_u31(order, a.div_group), unit = fp::fastdiv_u31(rest, a.div_tiles);
     const int batch = (int)fp::fastdiv_u31(unit, a.div_kvh), kvh = (int)unit - batch * a.KVH;
     const int head = kvh * a.group + (int)(order - rest * (uint32_t)a.group);
-    const int row0 = (a.tiles - 1 - (int)(rest - unit * (uint32_t)a.tiles)) * kRows;   // causal: the longest first
+    const int row0 = (a.tiles - 1 - (int)(rest - unit * (uint32_t)a.tiles)) * BM;   // causal: the longest first
     const int row = row0 + wave * 32 + (lane & 31), row_in = min(row, a.T - 1);
 
     bf16x8 q[D / 16], d_o[D / 16];
@@ -49,9 +50,9 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dq_ke
         delta = __uint_as_float(both[0]) + __uint_as_float(both[1]);
     }
     if constexpr (PADDED) {   // the chunks behind hd are never loaded
-        for (int i = tid; i < 4 * TILE / 16; i += kWaves * 64) reinterpret_cast<u32x4*>(tiles)[i] = u32x4{0, 0, 0, 0};
+        for (int i = tid; i < 4 * TILE / 16; i += NW * 64) reinterpret_cast<u32x4*>(tiles)[i] = u32x4{0, 0, 0, 0};
     }
-    const Spans spans = find_spans<kRows>(a, batch, row0, row0 + wave * 32);
+    const Spans spans = find_spans<BM>(a, batch, row0, row0 + wave * 32, true, !a.causal);
     Span mine = spans.mine;
     int low = 0, high = -1;
     if (spans.from <= spans.to) {
@@ -62,7 +63,7 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dq_ke
     if (a.causal && there) mine.last = row;
     const WaveSight sight = wave_sight(mine);
     if (!there) lse = delta = 0.0f;
-    if (row < a.T && lane < 32) {
+    if (row < a.T && lane < 32 && turn == 0) {
         a.stats[stat] = lse;
         a.stats[(int64_t)a.H * a.T * a.batch + stat] = delta;
     }
@@ -75,7 +76,7 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dq_ke
 
     const char* k = a.k + batch * a.k_sb + kvh * a.k_sh;
     const char* v = a.v + batch * a.v_sb + kvh * a.v_sh;
-    TileLoads<D, BN, kWaves, PADDED> k_loads, v_loads;
+    TileLoads<D, BN, NW, PADDED> k_loads, v_loads;
     k_loads.init(a.k_st);
     v_loads.init(a.v_st);
     const unsigned plain = R::plain_base(), turned = R::turned_base();
@@ -85,6 +86,7 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dq_ke
     };
     bool left_out = false;
     const auto at_edge = [&](int p) { return p < sight.full_from || p + 31 > sight.full_to; };
+    const auto mine_at_edge = [&](int p) { return (p - low) / 32 % H == turn && at_edge(p); };
     const auto take = [&](int p, unsigned kt, unsigned vt) {
         const bool edge = at_edge(p);
         f32x16 x[1], y[1];
@@ -113,36 +115,42 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 2 : 1) void attention_dq_ke
         wait_loads();
         __syncthreads();   // every wave's loads of this tile have landed, and its reads of the other set are done
         if (p + BN <= high) issue(p + BN, set ^ 1);
-        for (int u = 0; u < BN; u += 32)
+        for (int u = 32 * turn; u < BN; u += 32 * H)
             if (sight.any && p + u + 32 > sight.low && p + u <= sight.high)
                 take(p + u, lds + set * TILE + u * R::BYTES, lds + (2 + set) * TILE + u * R::BYTES);
     }
 
     // a logit of -infinity has a ds of 0, and 0 times an infinity is NaN
-    if (left_out) add_left_out<D, 32, true>(dq, k, a.k_st, low, high, mine, a.hd, at_edge);
-    if (row >= a.T) return;
+    if (left_out) add_left_out<D, 32, true>(dq, k, a.k_st, low, high, mine, a.hd, mine_at_edge);
+    if constexpr (H > 1) {
+        static_assert((H - 1) * RW * 128 * D <= 4 * TILE, "the sums fit the tiles");
+        sum_up<D, RW, H>(dq, 0, wave, turn, tiles);
+    }
+    if (row >= a.T || turn > 0) return;
     if (!there) {
 #pragma unroll
         for (int t = 0; t < D / 32; ++t)
 #pragma unroll
             for (int i = 0; i < 16; ++i) dq[t][i] = 0.0f;
     }
-    store_turned<D>(a.dq + (((int64_t)batch * a.H + head) * a.T + row) * a.hd, true, dq, a.scale, a.hd);
+    store_turned<D>(a.dq + (((int64_t)batch * a.H + head) * a.T + row) * a.hd, dq, a.scale, a.hd);
 }
 
-// Shapes of a workgroup: R rows of waves with 32 keys each, and H waves a row that share these keys and
-// take 32 tokens in turn of each tile of 32 H; their sums are added at the end.
-template <int D, bool PADDED, int RW, int H>
-__global__ __launch_bounds__(64 * RW * H, 1) void attention_dkv_kernel(AttentionArgs a) {
+// Shapes of a workgroup: RW rows of waves with 32 keys each, and H waves a row that share these keys and
+// take S times 32 tokens in turn of each tile of 32 H S; their sums are added at the end. Heads above 128: two
+// waves have the same keys and tokens, and every other 32 elements of dk and dv (PARTS); both
+// compute P and ds. One wave with all of them has no registers for a second on its SIMD, and at 256 not for itself.
+template <int D, bool PADDED, int RW, int H, int S, int PARTS>
+__global__ __launch_bounds__(64 * RW * H * PARTS, RW * H * PARTS == 4 && D <= 96 ? 2 : 1) void attention_dkv_kernel(AttentionArgs a) {
     using R = Rows<D>;
     // Heads of 128 and more: the accumulators, k and v leave no registers for two waves a SIMD (heads above 128: for one), so v's rows
     // stay in LDS.
     constexpr bool V_IN_LDS = D >= 128;
-    constexpr int NW = RW * H, BM = 32 * RW, BN = 32 * H, TILE = BN * R::BYTES;
+    constexpr int NW = RW * H * PARTS, BM = 32 * RW, BN = 32 * H * S, TILE = BN * R::BYTES, T = D / 32 / PARTS;
     __shared__ __attribute__((aligned(1024))) unsigned char tiles[4 * TILE + (V_IN_LDS ? BM * R::BYTES : 0)];   // q, q, do, do, v
     __shared__ __attribute__((aligned(16))) float stats[2][2][BN];             // set; lse log2(e), D; token
     const int tid = threadIdx.x, lane = tid & 63, place = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wave = place % RW, turn = place / RW;
+    const int wave = place % RW, turn = H > 1 ? place / RW % H : 0, part = PARTS > 1 ? place / (RW * H) : 0;
     const unsigned lds = (unsigned)(size_t)(lds_void*)tiles;
     const uint32_t order = in_xcd_order(blockIdx.x, a.blocks);
     const uint32_t unit = fp::fastdiv_u31(order, a.div_tiles);
@@ -157,7 +165,7 @@ __global__ __launch_bounds__(64 * RW * H, 1) void attention_dkv_kernel(Attention
     if constexpr (PADDED) {   // the chunks behind hd are never loaded
         for (int i = tid; i < (int)sizeof(tiles) / 16; i += NW * 64) reinterpret_cast<u32x4*>(tiles)[i] = u32x4{0, 0, 0, 0};
     }
-    const Spans spans = find_spans<BM>(a, batch, row0, row0 + wave * 32);
+    const Spans spans = find_spans<BM>(a, batch, row0, row0 + wave * 32, !a.causal, true);
     Span mine = spans.mine;   // the tokens that see this lane's key
     int low = 0, high = -1;
     if (spans.from <= spans.to) {
@@ -168,30 +176,30 @@ __global__ __launch_bounds__(64 * RW * H, 1) void attention_dkv_kernel(Attention
     if (a.causal && there) mine.first = row;
     const WaveSight sight = wave_sight(mine);
 
-    f32x16 dk[D / 32], dv[D / 32];
+    f32x16 dk[T], dv[T];
 #pragma unroll
-    for (int t = 0; t < D / 32; ++t)
+    for (int t = 0; t < T; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) dk[t][i] = dv[t][i] = 0.0f;
 
     TileLoads<D, BN, NW, PADDED, D < 128> q_loads, do_loads;
     q_loads.init(a.q_st);
     do_loads.init(a.o_st);
-    const unsigned plain = R::plain_base(), turned = R::turned_base();
-    // threads 0 .. BN - 1 fetch lse, BN .. 2 BN - 1 fetch D of the next tile
-    const auto issue = [&](int g, int p, int set) -> float {
+    const unsigned plain = R::plain_base(), turned = R::turned_base(part);
+    const auto issue = [&](int g, int p, int set) {
         const int head = kvh * a.group + g, count = high + 1 - p;
-        float s = 0.0f;
-        if (tid < 2 * BN) {
-            const int64_t at = ((int64_t)batch * a.H + head) * a.T + p + min(tid & (BN - 1), count - 1);
-            s = a.stats[(tid < BN ? 0 : (int64_t)a.H * a.T * a.batch) + at];
-        }
         q_loads.issue(a.q + batch * a.q_sb + head * a.q_sh + (int64_t)p * a.q_st, a.q_st, lds + set * TILE, count, a.hd);
         do_loads.issue(a.d_o + ((int64_t)batch * a.T + p) * a.o_st + (int64_t)head * a.hd * 2, a.o_st, lds + (2 + set) * TILE, count, a.hd);
-        return s;
-    };
-    const auto keep = [&](int set, float s) {
-        if (tid < 2 * BN) stats[set][tid / BN][tid & (BN - 1)] = s;
+        // a number a lane: BN of lse, then BN of D
+        static_assert(2 * BN % 64 == 0 && 2 * BN <= 64 * NW, "whole waves");
+        if (place * 64 < 2 * BN) {
+            int at = threadIdx.x;
+            asm volatile("" : "+v"(at));   // what follows from it is not kept since the last tile
+            const float* from = a.stats + (at < BN ? 0 : (int64_t)a.H * a.T * a.batch) + ((int64_t)batch * a.H + head) * a.T + p +
+                                min(at & (BN - 1), count - 1);
+            const unsigned dst = (unsigned)(size_t)(lds_void*)&stats[set][0][0] + (unsigned)place * 256;
+            asm volatile("s_nop 4\n\tglobal_load_lds_dword %0, off" ::"v"(from), "{m0}"(dst) : "memory");
+        }
     };
     bool left_out = false;
     const auto at_edge = [&](int p) { return p < sight.full_from || p + 31 > sight.full_to; };
@@ -199,7 +207,7 @@ __global__ __launch_bounds__(64 * RW * H, 1) void attention_dkv_kernel(Attention
     const auto take = [&](int p, unsigned qt, unsigned dt, const float* lse, const float* delta) {
         const bool edge = at_edge(p);
         f32x16 x[1], y[1];
-        constexpr int C = D / 32 % 2 == 0 && D >= 128 ? 2 : D / 32, J = D >= 128 ? 1 : 2;
+        constexpr int C = T == 4 && D >= 128 ? 2 : T, J = D >= 128 ? 1 : 2;
         bf16x8 w[2], dw[2];
         {
             const int h = lane >> 5;
@@ -230,9 +238,9 @@ __global__ __launch_bounds__(64 * RW * H, 1) void attention_dkv_kernel(Attention
             to_operands<1>(dw, y);
             __builtin_amdgcn_sched_barrier(0);
         }
-        left_out |= add_turned<D, 1, C>(dv, w, dt + turned, edge);
+        left_out |= add_turned<D, 1, C, PARTS>(dv, w, dt + turned, edge);
         // where a token's q is not finite neither is its lse, so that ds is NaN for every key that it sees
-        add_turned<D, 1, C>(dk, dw, qt + turned, edge);
+        add_turned<D, 1, C, PARTS>(dk, dw, qt + turned, edge);
     };
 
     if constexpr (PADDED) __syncthreads();
@@ -245,8 +253,7 @@ __global__ __launch_bounds__(64 * RW * H, 1) void attention_dkv_kernel(Attention
             v_loads.init(a.v_st);
             v_loads.issue(v_head + (int64_t)row0 * a.v_st, a.v_st, lds + 4 * TILE, min(BM, a.T - row0), a.hd);
         }
-        const float s = issue(0, low, 0);
-        keep(0, s);
+        issue(0, low, 0);
         int g = 0, p = low;
         while (g < a.group) {
             int next_g = g, next_p = p + BN;
@@ -256,12 +263,10 @@ __global__ __launch_bounds__(64 * RW * H, 1) void attention_dkv_kernel(Attention
             }
             wait_loads();
             __syncthreads();   // every wave's loads of this tile have landed, and its reads of the other set are done
-            float next = 0.0f;
-            if (next_g < a.group) next = issue(next_g, next_p, set ^ 1);
-            const int u = 32 * turn;
-            if (sight.any && p + u + 32 > sight.low && p + u <= sight.high)
-                take(p + u, lds + set * TILE + u * R::BYTES, lds + (2 + set) * TILE + u * R::BYTES, &stats[set][0][u], &stats[set][1][u]);
-            keep(set ^ 1, next);
+            if (next_g < a.group) issue(next_g, next_p, set ^ 1);
+            for (int u = 32 * turn; u < BN; u += 32 * H)
+                if (sight.any && p + u + 32 > sight.low && p + u <= sight.high)
+                    take(p + u, lds + set * TILE + u * R::BYTES, lds + (2 + set) * TILE + u * R::BYTES, &stats[set][0][u], &stats[set][1][u]);
             set ^= 1;
             g = next_g;
             p = next_p;
@@ -270,81 +275,78 @@ __global__ __launch_bounds__(64 * RW * H, 1) void attention_dkv_kernel(Attention
 
     if (left_out)
         for (int g = 0; g < a.group; ++g)
-            add_left_out<D, 32, false>(dv, a.d_o + (int64_t)batch * a.T * a.o_st + (int64_t)(kvh * a.group + g) * a.hd * 2, a.o_st, low, high,
-                                       mine, a.hd, mine_at_edge);
+            add_left_out<D, 32, false, PARTS>(dv, a.d_o + (int64_t)batch * a.T * a.o_st + (int64_t)(kvh * a.group + g) * a.hd * 2, a.o_st, low, high,
+                                       mine, a.hd, mine_at_edge, part);
     if constexpr (H > 1) {
-        // a row's sums: its first wave takes dk, its second dv, from what the others leave in the tiles' place
-        f32x4* const shared = reinterpret_cast<f32x4*>(tiles) + wave * D * 8 + lane;
-        constexpr int NEXT = RW * D * 8;   // the next wave of the row
-        const auto sum_up = [&](f32x16 (&y)[D / 32], int taker) {
-            __syncthreads();   // the tiles, or the last sums, are read
-            if (turn != taker) {
-                f32x4* const to = shared + (turn > taker ? turn - 1 : turn) * NEXT;
-#pragma unroll
-                for (int j = 0; j < D / 8; ++j)
-                    to[j * 64] = f32x4{y[j >> 2][4 * (j & 3)], y[j >> 2][4 * (j & 3) + 1], y[j >> 2][4 * (j & 3) + 2], y[j >> 2][4 * (j & 3) + 3]};
-            }
-            __syncthreads();
-            if (turn == taker) {
-#pragma unroll
-                for (int g = 0; g < H - 1; ++g)
-#pragma unroll
-                    for (int j = 0; j < D / 8; ++j) {
-                        const f32x4 x = shared[g * NEXT + j * 64];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) y[j >> 2][4 * (j & 3) + i] += x[i];
-                    }
-            }
-        };
-        static_assert((H - 1) * NEXT * 16 <= 4 * TILE, "the sums fit the tiles");
-        sum_up(dk, 0);
-        sum_up(dv, 1);
+        static_assert((H - 1) * RW * 128 * D <= 4 * TILE, "the sums fit the tiles");
+        sum_up<D / PARTS, RW * PARTS, H>(dk, 0, part * RW + wave, turn, tiles);
+        sum_up<D / PARTS, RW * PARTS, H>(dv, 1, part * RW + wave, turn, tiles);
     }
     if (row >= a.T) return;
     const int64_t to = (((int64_t)batch * a.KVH + kvh) * a.T + row) * a.hd;
-    const auto store = [&](__bf16* out, f32x16 (&y)[D / 32], float by) {
+    const auto store = [&](__bf16* out, f32x16 (&y)[T], float by) {
         if (!there) {
 #pragma unroll
-            for (int t = 0; t < D / 32; ++t)
+            for (int t = 0; t < T; ++t)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) y[t][i] = 0.0f;
         }
-        store_turned<D>(out + to, true, y, by, a.hd);
+        store_turned<D, PARTS>(out + to, y, by, a.hd, part);
     };
     if (H == 1 || turn == 0) store(a.dk, dk, a.scale);
     if (H == 1 || turn == 1) store(a.dv, dv, 1.0f);
 }
 
-template <int D, int RW, int H>
+template <int D, int RW, int H, int S, int PARTS = 1>
 void launch_dkv(const prompt_attention_desc& d, AttentionArgs a, hipStream_t st) {
     a.tiles = (int32_t)((d.tokens + 32 * RW - 1) / (32 * RW));
     a.div_tiles = fp::make_fastdiv_u31((uint32_t)a.tiles);
     a.blocks = (uint32_t)(d.batch * a.KVH * a.tiles);
     if (d.head_dim == D)
-        hipLaunchKernelGGL((attention_dkv_kernel<D, false, RW, H>), dim3(a.blocks), dim3(64 * RW * H), 0, st, a);
+        hipLaunchKernelGGL((attention_dkv_kernel<D, false, RW, H, S, PARTS>), dim3(a.blocks), dim3(64 * RW * H * PARTS), 0, st, a);
     else
-        hipLaunchKernelGGL((attention_dkv_kernel<D, true, RW, H>), dim3(a.blocks), dim3(64 * RW * H), 0, st, a);
+        hipLaunchKernelGGL((attention_dkv_kernel<D, true, RW, H, S, PARTS>), dim3(a.blocks), dim3(64 * RW * H * PARTS), 0, st, a);
+}
+
+template <int D, int RW, int H, int S>
+void launch_dq(const prompt_attention_desc& d, AttentionArgs a, hipStream_t st) {
+    a.tiles = (int32_t)((d.tokens + 32 * RW - 1) / (32 * RW));
+    a.div_tiles = fp::make_fastdiv_u31((uint32_t)a.tiles);
+    a.blocks = (uint32_t)(d.batch * d.n_heads * a.tiles);
+    if (d.head_dim == D)
+        hipLaunchKernelGGL((attention_dq_kernel<D, false, RW, H, S>), dim3(a.blocks), dim3(64 * RW * H), 0, st, a);
+    else
+        hipLaunchKernelGGL((attention_dq_kernel<D, true, RW, H, S>), dim3(a.blocks), dim3(64 * RW * H), 0, st, a);
 }
 
 template <int D>
 void launch(const prompt_attention_desc& d, AttentionArgs a, hipStream_t st) {
-    a.tiles = (int32_t)((d.tokens + kRows - 1) / kRows);
-    a.div_tiles = fp::make_fastdiv_u31((uint32_t)a.tiles);
-    a.blocks = (uint32_t)(d.batch * d.n_heads * a.tiles);
-    if (d.head_dim == D)
-        hipLaunchKernelGGL((attention_dq_kernel<D, false>), dim3(a.blocks), dim3(kWaves * 64), 0, st, a);
-    else
-        hipLaunchKernelGGL((attention_dq_kernel<D, true>), dim3(a.blocks), dim3(kWaves * 64), 0, st, a);
-    // workgroups of 128 keys
-    const int64_t blocks = d.batch * a.KVH * ((d.tokens + 127) / 128);
+    // workgroups of 128 tokens
+    const int64_t blocks = d.batch * d.n_heads * ((d.tokens + 127) / 128);
     if constexpr (D > 128)
-        launch_dkv<D, 4, 1>(d, a, st);
-    else if (blocks < kFewBlocks)
-        launch_dkv<D, 2, 4>(d, a, st);
-    else if (D == 128 || blocks < kManyBlocks)
-        launch_dkv<D, 4, 2>(d, a, st);
+        launch_dq<D, 4, 1, 1>(d, a, st);
+    else if (fp::few_workgroups(blocks, d))
+        launch_dq<D, 2, 4, 1>(d, a, st);
     else
-        launch_dkv<D <= 96 ? D : 96, 4, 1>(d, a, st);
+        launch_dq<D, 4, 1, 2>(d, a, st);
+    // Workgroups of 128 keys are few for longer than those of tokens: a group's heads are in one, and with a causal mask the first
+    // has twice the mean's work. dq and dk, dv, heads of 64, us, with 4 rows of one wave / 4 of 2 / 2 of 4 (dq as it is best):
+    //   4 x 512 tokens, 12 heads (192 workgroups)    - / 36 / 41        8 x 512, 12 heads (384)  46 / 52 / -
+    //   16 x 2048 (256)     108 / 94 / 100           causal             108 / 78 / 66
+    //   32 x 2048 (512)     147 / 157 / 174          causal             133 / 136 / 129       16 x 4096, causal  236 / 194 / 205
+    // Heads of 128 have registers for one wave a SIMD of 4 rows of one, and take two.
+    const int64_t kv_blocks = d.batch * a.KVH * ((d.tokens + 127) / 128);
+    const int64_t few = d.tokens < 1024 ? 160 : d.causal ? 512 : 256;
+    if constexpr (D == 256)
+        launch_dkv<D, 2, 1, 1, 2>(d, a, st);
+    else if constexpr (D == 192)
+        launch_dkv<D, 2, 2, 1, 2>(d, a, st);
+    else if (kv_blocks < few)
+        launch_dkv<D, 2, 4, 1>(d, a, st);
+    else if (D == 128 || kv_blocks < 2 * few)
+        launch_dkv<D, 4, 2, 1>(d, a, st);
+    else
+        launch_dkv<D <= 96 ? D : 96, 4, 1, 2>(d, a, st);
 }
 
 }  // namespace

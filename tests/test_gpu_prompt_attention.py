@@ -94,6 +94,11 @@ CASES += [
     # groups
     dict(batch=2, tokens=90, heads=12, kvh=1, hd=32), dict(batch=2, tokens=131, heads=6, kvh=3, hd=128, layout="qkv"),
     dict(batch=1, tokens=700, heads=4, kvh=1, hd=64), dict(batch=1, tokens=1100, heads=2, kvh=2, hd=128, causal=False),
+    # many heads: workgroups of other shapes than the small calls above have
+    *(dict(batch=2, tokens=131, heads=128, kvh=128, hd=hd, causal=c) for hd, c in ((32, True), (64, False), (64, True), (80, True), (96, False), (128, True), (104, False))),
+    *(dict(batch=2, tokens=150, heads=128, kvh=64, hd=hd, causal=c, extents=[150, 97]) for hd, c in ((16, True), (64, False), (72, True), (128, False), (120, True))),
+    dict(batch=1, tokens=515, heads=128, kvh=128, hd=64, sequences=5, extents=[2, 60, 260, 261, 400, 513]),
+    dict(batch=1, tokens=515, heads=128, kvh=64, hd=128, sequences=5, extents=[2, 60, 260, 261, 400, 513], causal=False),
     # steep and flat
     dict(batch=1, tokens=150, heads=2, kvh=2, hd=64, scale=3.0), dict(batch=1, tokens=150, heads=2, kvh=2, hd=64, scale=1e-6),
 ]
@@ -118,7 +123,9 @@ def test_maxima_that_move():
 @pytest.mark.parametrize("kw", [dict(batch=1, tokens=150, heads=2, kvh=1, hd=64), dict(batch=1, tokens=150, heads=2, kvh=1, hd=80, causal=False),
                                 dict(batch=1, tokens=170, heads=2, kvh=1, hd=128, sequences=4, extents=[3, 40, 90, 90, 160]),
                                 dict(batch=2, tokens=140, heads=1, kvh=1, hd=64, extents=[100, 37]),
-                                dict(batch=1, tokens=150, heads=2, kvh=2, hd=256, sequences=2, extents=[0, 77, 150], causal=False)])
+                                dict(batch=1, tokens=150, heads=2, kvh=2, hd=256, sequences=2, extents=[0, 77, 150], causal=False),
+                                dict(batch=1, tokens=150, heads=256, kvh=128, hd=128, extents=[133]),
+                                dict(batch=1, tokens=150, heads=256, kvh=256, hd=64, sequences=2, extents=[0, 77, 141])])
 @pytest.mark.parametrize("which", ["v", "k", "q", "do"])
 def test_what_is_not_finite_reaches_those_that_see_it(kw, which):
     print(f"[case] attention {which} {kw}", flush=True)
