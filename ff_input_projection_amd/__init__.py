@@ -43,8 +43,9 @@ KV_CACHE_SYMBOLS = ["kv_cache_validate", "kv_cache_create", "kv_cache_storage_by
 ROPE_SYMBOLS = ["rope_validate", "rope_create", "rope_split", "rope_split_backward", "rope_rotate",
                 "rope_rotate_backward", "rope_destroy"]
 # include/prompt_attention.h
-PROMPT_ATTENTION_SYMBOLS = ["prompt_attention_validate", "prompt_attention_create", "prompt_attention_workspace_size",
-                            "prompt_attention_run", "prompt_attention_backward", "prompt_attention_destroy"]
+PROMPT_ATTENTION_SYMBOLS = ["prompt_attention_validate", "prompt_attention_create", "prompt_attention_run",
+                            "prompt_attention_backward_workspace_size", "prompt_attention_backward",
+                            "prompt_attention_destroy"]
 
 OK, EINVAL, EUNSUPPORTED, EALIGN, EALIAS, EHIP, ESCRATCH = 0, -1, -2, -3, -4, -5, -6
 BF16, F32 = 0, 1
@@ -207,8 +208,8 @@ def load_library():
         getattr(lib, name).restype = ctypes.c_int
     lib.prompt_attention_validate.argtypes = [ctypes.POINTER(PromptAttentionDesc)]
     lib.prompt_attention_create.argtypes = [ctypes.POINTER(PromptAttentionDesc), ctypes.POINTER(vp)]
-    lib.prompt_attention_workspace_size.argtypes = [vp, size_p, size_p]
-    lib.prompt_attention_run.argtypes = [vp] * 8 + [ctypes.c_size_t, vp]
+    lib.prompt_attention_run.argtypes = [vp] * 8
+    lib.prompt_attention_backward_workspace_size.argtypes = [vp, size_p]
     lib.prompt_attention_backward.argtypes = [vp] * 12 + [ctypes.c_size_t, vp]
     lib.prompt_attention_destroy.argtypes = [vp]
     for name in PROMPT_ATTENTION_SYMBOLS:

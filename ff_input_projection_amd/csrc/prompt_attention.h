@@ -27,6 +27,8 @@ struct AttentionArgs {
     const float* lse_in;
     __bf16 *dq, *dk, *dv;
     float* stats;                // backward: [b*H, T] lse log2(e), then [b*H, T] D
+    float* partial;              // backward: [kv_parts][dk, dv][b, KVH, T, hd], where kv_parts > 1
+    int32_t part_heads;          // heads of a group that a workgroup of keys passes over
     int64_t q_sb, q_sh, k_sb, k_sh, v_sb, v_sh;   // bytes
     uint32_t q_st, k_st, v_st, o_st;              // bytes between tokens
     int32_t batch, T, H, KVH, hd, group, sequences, causal;
@@ -39,7 +41,8 @@ struct AttentionArgs {
 struct AttentionPlan {
     int32_t dim = 0;             // the kernels' head size, hd or the next one that is compiled
     int64_t rows = 0;            // b T H
-    size_t run_workspace = 0, backward_workspace = 0;
+    int32_t kv_parts = 1;        // parts that a group's heads are cut into for dk and dv
+    size_t backward_workspace = 0;
 };
 
 // Whether workgroups of 128 tokens (4 waves, two workgroups a CU) are so few, or with a causal mask so different, that
@@ -54,6 +57,8 @@ inline bool few_workgroups(int64_t blocks, const prompt_attention_desc& d) {
     return d.tokens > 128 && (blocks < 256 || (d.tokens >= 1024 && blocks < (d.causal && d.head_dim <= 64 ? 768 : 512)));
 }
 
+// Sets kv_parts.
+void plan_attention_backward(const prompt_attention_desc& d, int64_t kvh, AttentionPlan* p);
 hipError_t launch_attention(const prompt_attention_desc& d, const AttentionPlan& p, AttentionArgs a, hipStream_t st);
 hipError_t launch_attention_backward(const prompt_attention_desc& d, const AttentionPlan& p, AttentionArgs a, hipStream_t st);
 

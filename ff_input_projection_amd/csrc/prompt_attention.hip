@@ -227,6 +227,9 @@ int64_t extent(const int64_t (&s)[3], int64_t b, int64_t heads, int64_t tokens, 
     return (b - 1) * s[0] + (heads - 1) * s[1] + (tokens - 1) * s[2] + hd;
 }
 
+// What the backward pass keeps of each token and head, in whole pieces of 16 bytes.
+size_t stats_bytes(const fp::AttentionPlan& p) { return ((size_t)p.rows * 8 + 15) / 16 * 16; }
+
 int check(const prompt_attention_desc* d, fp::AttentionPlan* out, int64_t* kvh_out) {
     if (!d) return FUSED_PROJ_EINVAL;
     if (d->dtype != FUSED_PROJ_BF16 && d->dtype != FUSED_PROJ_F32) return FUSED_PROJ_EINVAL;
@@ -261,7 +264,9 @@ int check(const prompt_attention_desc* d, fp::AttentionPlan* out, int64_t* kvh_o
             break;
         }
     p.rows = d->batch * d->tokens * d->n_heads;
-    p.backward_workspace = (size_t)p.rows * 8;
+    fp::plan_attention_backward(*d, kvh, &p);
+    p.backward_workspace = stats_bytes(p);
+    if (p.kv_parts > 1) p.backward_workspace += (size_t)p.kv_parts * 2 * (size_t)(d->batch * kvh * d->tokens * d->head_dim) * 4;
     if (out) *out = p;
     if (kvh_out) *kvh_out = kvh;
     return FUSED_PROJ_OK;
@@ -358,23 +363,21 @@ int prompt_attention_create(const prompt_attention_desc* desc, prompt_attention_
     return FUSED_PROJ_OK;
 }
 
-int prompt_attention_workspace_size(prompt_attention_t h, size_t* run, size_t* backward) {
-    if (!h || !run || !backward) return FUSED_PROJ_EINVAL;
-    *run = h->p.run_workspace;
-    *backward = h->p.backward_workspace;
+int prompt_attention_backward_workspace_size(prompt_attention_t h, size_t* bytes) {
+    if (!h || !bytes) return FUSED_PROJ_EINVAL;
+    *bytes = h->p.backward_workspace;
     return FUSED_PROJ_OK;
 }
 
 int prompt_attention_run(prompt_attention_t h, const void* q, const void* k, const void* v, const int32_t* extents, void* o,
-                         void* lse, void* workspace, size_t workspace_bytes, void* stream) {
+                         void* lse, void* stream) {
     if (!h) return FUSED_PROJ_EINVAL;
     if (h->p.rows == 0) return FUSED_PROJ_OK;
-    const size_t need = h->p.run_workspace;
-    if (!o || (need > 0 && (!workspace || workspace_bytes < need))) return FUSED_PROJ_EINVAL;
-    if ((uintptr_t)o & 15u || (uintptr_t)lse & 3u || (need > 0 && (uintptr_t)workspace & 15u)) return FUSED_PROJ_EALIGN;
-    Range r[3] = {range(o, h->p.rows * h->d.head_dim * 2), range(lse, lse ? h->p.rows * 4 : 0), range(workspace, (int64_t)need)};
+    if (!o) return FUSED_PROJ_EINVAL;
+    if ((uintptr_t)o & 15u || (uintptr_t)lse & 3u) return FUSED_PROJ_EALIGN;
+    Range r[2] = {range(o, h->p.rows * h->d.head_dim * 2), range(lse, lse ? h->p.rows * 4 : 0)};
     AttentionArgs a;
-    const int rc = prepare(h, q, k, v, extents, r, 3, 3, &a);
+    const int rc = prepare(h, q, k, v, extents, r, 2, 2, &a);
     if (rc) return rc;
     a.o = static_cast<__bf16*>(o);
     a.lse = static_cast<float*>(lse);
@@ -403,6 +406,7 @@ int prompt_attention_backward(prompt_attention_t h, const void* q, const void* k
     a.dk = static_cast<__bf16*>(dk);
     a.dv = static_cast<__bf16*>(dv);
     a.stats = static_cast<float*>(workspace);
+    a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + stats_bytes(h->p));
     return hip_status(fp::launch_attention_backward(h->d, h->p, a, static_cast<hipStream_t>(stream)));
 }
 

@@ -158,6 +158,8 @@ __global__ __launch_bounds__(64 * RW * H * PARTS, RW * H * PARTS == 4 && D <= 96
     const int row0 = (int)(order - unit * (uint32_t)a.tiles) * BM;   // causal: the first keys are seen by most
     const int row = row0 + wave * 32 + (lane & 31), row_in = min(row, a.T - 1);
 
+    const int first_head = (int)blockIdx.y * a.part_heads, behind_head = min(first_head + a.part_heads, a.group);   // of the group
+
     bf16x8 k[D / 16], v[V_IN_LDS ? 1 : D / 16];
     load_rows<D>(k, a.k + batch * a.k_sb + kvh * a.k_sh + (int64_t)row_in * a.k_st, row < a.T, a.hd);
     const char* v_head = a.v + batch * a.v_sb + kvh * a.v_sh;
@@ -253,9 +255,9 @@ __global__ __launch_bounds__(64 * RW * H * PARTS, RW * H * PARTS == 4 && D <= 96
             v_loads.init(a.v_st);
             v_loads.issue(v_head + (int64_t)row0 * a.v_st, a.v_st, lds + 4 * TILE, min(BM, a.T - row0), a.hd);
         }
-        issue(0, low, 0);
-        int g = 0, p = low;
-        while (g < a.group) {
+        issue(first_head, low, 0);
+        int g = first_head, p = low;
+        while (g < behind_head) {
             int next_g = g, next_p = p + BN;
             if (next_p > high) {
                 next_p = low;
@@ -263,7 +265,7 @@ __global__ __launch_bounds__(64 * RW * H * PARTS, RW * H * PARTS == 4 && D <= 96
             }
             wait_loads();
             __syncthreads();   // every wave's loads of this tile have landed, and its reads of the other set are done
-            if (next_g < a.group) issue(next_g, next_p, set ^ 1);
+            if (next_g < behind_head) issue(next_g, next_p, set ^ 1);
             for (int u = 32 * turn; u < BN; u += 32 * H)
                 if (sight.any && p + u + 32 > sight.low && p + u <= sight.high)
                     take(p + u, lds + set * TILE + u * R::BYTES, lds + (2 + set) * TILE + u * R::BYTES, &stats[set][0][u], &stats[set][1][u]);
@@ -274,7 +276,7 @@ __global__ __launch_bounds__(64 * RW * H * PARTS, RW * H * PARTS == 4 && D <= 96
     }
 
     if (left_out)
-        for (int g = 0; g < a.group; ++g)
+        for (int g = first_head; g < behind_head; ++g)
             add_left_out<D, 32, false, PARTS>(dv, a.d_o + (int64_t)batch * a.T * a.o_st + (int64_t)(kvh * a.group + g) * a.hd * 2, a.o_st, low, high,
                                        mine, a.hd, mine_at_edge, part);
     if constexpr (H > 1) {
@@ -291,21 +293,55 @@ __global__ __launch_bounds__(64 * RW * H * PARTS, RW * H * PARTS == 4 && D <= 96
 #pragma unroll
                 for (int i = 0; i < 16; ++i) y[t][i] = 0.0f;
         }
-        store_turned<D, PARTS>(out + to, y, by, a.hd, part);
+        if (a.partial) {
+            float* const sums = a.partial + ((int64_t)blockIdx.y * 2 + (out == a.dv)) * ((int64_t)a.batch * a.KVH * a.T * a.hd) + to;
+#pragma unroll
+            for (int i = 0; i < 4 * T; ++i) {
+                const int d = 32 * ((i >> 2) * PARTS + part) + 8 * (i & 3) + 4 * (lane >> 5);
+                if (d < a.hd)
+                    *reinterpret_cast<f32x4*>(sums + d) = f32x4{y[i >> 2][4 * (i & 3)], y[i >> 2][4 * (i & 3) + 1], y[i >> 2][4 * (i & 3) + 2], y[i >> 2][4 * (i & 3) + 3]};
+            }
+        } else {
+            store_turned<D, PARTS>(out + to, y, by, a.hd, part);
+        }
     };
     if (H == 1 || turn == 0) store(a.dk, dk, a.scale);
     if (H == 1 || turn == 1) store(a.dv, dv, 1.0f);
 }
 
+// Workgroups of 128 keys are few for longer than those of tokens: a group's heads are in one, and with a causal mask the first
+// has twice the mean's work. dq and dk, dv, heads of 64, us, with 4 rows of one wave / 4 of 2 / 2 of 4 (dq as it is best):
+//   4 x 512 tokens, 12 heads (192 workgroups)    - / 36 / 41        8 x 512, 12 heads (384)  46 / 52 / -
+//   16 x 2048 (256)     108 / 94 / 100           causal             108 / 78 / 66
+//   32 x 2048 (512)     147 / 157 / 174          causal             133 / 136 / 129       16 x 4096, causal  236 / 194 / 205
+// Heads of 128 have registers for one wave a SIMD of 4 rows of one, and take two.
+int64_t few_key_blocks(const prompt_attention_desc& d) { return d.tokens < 1024 ? 160 : d.causal ? 512 : 256; }
+
+// Adds up the parts of dk and dv, 4 elements a thread.
+__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, int parts, int64_t n) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    const int dv = blockIdx.y;
+    const float* from = a.partial + dv * n + i;
+    f32x4 sum = *reinterpret_cast<const f32x4*>(from);
+    for (int p = 1; p < parts; ++p) sum += *reinterpret_cast<const f32x4*>(from + (int64_t)p * 2 * n);
+    const float by = dv ? 1.0f : a.scale;
+    bf16x4 o;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = (__bf16)(sum[k] * by);
+    *reinterpret_cast<bf16x4*>((dv ? a.dv : a.dk) + i) = o;
+}
+
 template <int D, int RW, int H, int S, int PARTS = 1>
-void launch_dkv(const prompt_attention_desc& d, AttentionArgs a, hipStream_t st) {
+void launch_dkv(const prompt_attention_desc& d, const fp::AttentionPlan& p, AttentionArgs a, hipStream_t st) {
     a.tiles = (int32_t)((d.tokens + 32 * RW - 1) / (32 * RW));
     a.div_tiles = fp::make_fastdiv_u31((uint32_t)a.tiles);
     a.blocks = (uint32_t)(d.batch * a.KVH * a.tiles);
+    const dim3 grid(a.blocks, (unsigned)p.kv_parts);
     if (d.head_dim == D)
-        hipLaunchKernelGGL((attention_dkv_kernel<D, false, RW, H, S, PARTS>), dim3(a.blocks), dim3(64 * RW * H * PARTS), 0, st, a);
+        hipLaunchKernelGGL((attention_dkv_kernel<D, false, RW, H, S, PARTS>), grid, dim3(64 * RW * H * PARTS), 0, st, a);
     else
-        hipLaunchKernelGGL((attention_dkv_kernel<D, true, RW, H, S, PARTS>), dim3(a.blocks), dim3(64 * RW * H * PARTS), 0, st, a);
+        hipLaunchKernelGGL((attention_dkv_kernel<D, true, RW, H, S, PARTS>), grid, dim3(64 * RW * H * PARTS), 0, st, a);
 }
 
 template <int D, int RW, int H, int S>
@@ -320,7 +356,7 @@ void launch_dq(const prompt_attention_desc& d, AttentionArgs a, hipStream_t st) 
 }
 
 template <int D>
-void launch(const prompt_attention_desc& d, AttentionArgs a, hipStream_t st) {
+void launch(const prompt_attention_desc& d, const fp::AttentionPlan& p, AttentionArgs a, hipStream_t st) {
     // workgroups of 128 tokens
     const int64_t blocks = d.batch * d.n_heads * ((d.tokens + 127) / 128);
     if constexpr (D > 128)
@@ -329,39 +365,51 @@ void launch(const prompt_attention_desc& d, AttentionArgs a, hipStream_t st) {
         launch_dq<D, 2, 4, 1>(d, a, st);
     else
         launch_dq<D, 4, 1, 2>(d, a, st);
-    // Workgroups of 128 keys are few for longer than those of tokens: a group's heads are in one, and with a causal mask the first
-    // has twice the mean's work. dq and dk, dv, heads of 64, us, with 4 rows of one wave / 4 of 2 / 2 of 4 (dq as it is best):
-    //   4 x 512 tokens, 12 heads (192 workgroups)    - / 36 / 41        8 x 512, 12 heads (384)  46 / 52 / -
-    //   16 x 2048 (256)     108 / 94 / 100           causal             108 / 78 / 66
-    //   32 x 2048 (512)     147 / 157 / 174          causal             133 / 136 / 129       16 x 4096, causal  236 / 194 / 205
-    // Heads of 128 have registers for one wave a SIMD of 4 rows of one, and take two.
-    const int64_t kv_blocks = d.batch * a.KVH * ((d.tokens + 127) / 128);
-    const int64_t few = d.tokens < 1024 ? 160 : d.causal ? 512 : 256;
+    const int64_t kv_blocks = blocks / a.group, few = few_key_blocks(d);
     if constexpr (D == 256)
-        launch_dkv<D, 2, 1, 1, 2>(d, a, st);
+        launch_dkv<D, 2, 1, 1, 2>(d, p, a, st);
     else if constexpr (D == 192)
-        launch_dkv<D, 2, 2, 1, 2>(d, a, st);
+        launch_dkv<D, 2, 2, 1, 2>(d, p, a, st);
     else if (kv_blocks < few)
-        launch_dkv<D, 2, 4, 1>(d, a, st);
+        launch_dkv<D, 2, 4, 1>(d, p, a, st);
     else if (D == 128 || kv_blocks < 2 * few)
-        launch_dkv<D, 4, 2, 1>(d, a, st);
+        launch_dkv<D, 4, 2, 1>(d, p, a, st);
     else
-        launch_dkv<D <= 96 ? D : 96, 4, 1, 2>(d, a, st);
+        launch_dkv<D <= 96 ? D : 96, 4, 1, 2>(d, p, a, st);
 }
 
 }  // namespace
 
 namespace fp {
 
-hipError_t launch_attention_backward(const prompt_attention_desc& d, const AttentionPlan& p, AttentionArgs a, hipStream_t st) {
-    switch (p.dim) {
-        case 32: launch<32>(d, a, st); break;
-        case 64: launch<64>(d, a, st); break;
-        case 96: launch<96>(d, a, st); break;
-        case 128: launch<128>(d, a, st); break;
-        case 192: launch<192>(d, a, st); break;
-        default: launch<256>(d, a, st);
+void plan_attention_backward(const prompt_attention_desc& d, int64_t kvh, AttentionPlan* p) {
+    // Where the workgroups are of 64 keys and still fewer than twice the CUs (one is on a CU at a time), a group's heads are cut into parts;
+    // their sums go through memory. The whole backward pass, causal, without and with parts: 32 heads on 8 of 128, 512 tokens 60 and 44 us,
+    // 2048 tokens 222 and 182; 16 on 4 of 256, 1024 tokens 352 and 155.
+    const int64_t group = d.n_heads / kvh, blocks = d.batch * kvh * ((d.tokens + 63) / 64);
+    const bool small = p->dim > 128 || d.batch * kvh * ((d.tokens + 127) / 128) < few_key_blocks(d);
+    p->kv_parts = 1;
+    if (small && blocks > 0 && blocks < 512 && d.tokens >= 256) {
+        const int64_t wanted = (512 + blocks - 1) / blocks, heads = (group + wanted - 1) / wanted;
+        p->kv_parts = (int32_t)((group + heads - 1) / heads);
     }
+}
+
+hipError_t launch_attention_backward(const prompt_attention_desc& d, const AttentionPlan& p, AttentionArgs a, hipStream_t st) {
+    a.part_heads = (a.group + p.kv_parts - 1) / p.kv_parts;
+    if (p.kv_parts == 1) a.partial = nullptr;
+    switch (p.dim) {
+        case 32: launch<32>(d, p, a, st); break;
+        case 64: launch<64>(d, p, a, st); break;
+        case 96: launch<96>(d, p, a, st); break;
+        case 128: launch<128>(d, p, a, st); break;
+        case 192: launch<192>(d, p, a, st); break;
+        default: launch<256>(d, p, a, st);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.kv_parts == 1) return e;
+    const int64_t n = d.batch * a.KVH * d.tokens * d.head_dim;
+    hipLaunchKernelGGL(attention_join_kernel, dim3((unsigned)((n / 4 + 255) / 256), 2), dim3(256), 0, st, a, p.kv_parts, n);
     return hipGetLastError();
 }
 

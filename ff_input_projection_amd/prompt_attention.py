@@ -50,11 +50,11 @@ class PromptAttention:
         if rc != OK:
             raise FusedProjError(rc, "prompt_attention_create")
         self._h, self._device = h, torch.cuda.current_device()
-        run, back = ctypes.c_size_t(), ctypes.c_size_t()
-        rc = self._lib.prompt_attention_workspace_size(h, ctypes.byref(run), ctypes.byref(back))
+        n = ctypes.c_size_t()
+        rc = self._lib.prompt_attention_backward_workspace_size(h, ctypes.byref(n))
         if rc != OK:
-            raise FusedProjError(rc, "prompt_attention_workspace_size")
-        self._run_bytes, self._backward_bytes = int(run.value), int(back.value)
+            raise FusedProjError(rc, "prompt_attention_backward_workspace_size")
+        self._workspace_bytes = int(n.value)
         # [b*heads, T, hd], or [b, heads, T, hd] where a tensor has strides of its own
         self._shapes, self._strides = [], []
         for name, heads in (("q_strides", self.H), ("k_strides", self.KVH), ("v_strides", self.KVH)):
@@ -72,11 +72,11 @@ class PromptAttention:
         qkv = tuple(("in", s, t, bf16) for s, t in zip(self._shapes, self._strides))
         extents = ("maybe", self._extents_shape, None, torch.int32)
         self._forward = _planned_call("prompt_attention_run", h, (*qkv, extents, ("out", self._o_shape, bf16),
-                                                                  ("out", self._lse_shape, f32), ("workspace", self._run_bytes)))
+                                                                  ("out", self._lse_shape, f32)))
         self._backward = _planned_call(
             "prompt_attention_backward", h,
             (*qkv, extents, ("in", self._o_shape, None, bf16), ("in", self._lse_shape, None, f32),
-             ("in", self._o_shape, None, bf16), *(("out", s, bf16) for s in self._shapes), ("workspace", self._backward_bytes)))
+             ("in", self._o_shape, None, bf16), *(("out", s, bf16) for s in self._shapes), ("workspace", self._workspace_bytes)))
         self._call = _planned_call_function()
 
     @classmethod
@@ -93,8 +93,8 @@ class PromptAttention:
                    k_strides=k.stride()[:3], v_strides=v.stride()[:3], dtype=q.dtype, **kw)
 
     def workspace_bytes(self) -> int:
-        """Device workspace that serves a call and its backward pass (one after the other)."""
-        return max(self._run_bytes, self._backward_bytes)
+        """Device workspace the backward pass needs."""
+        return self._workspace_bytes
 
     def alloc_workspace(self, device) -> torch.Tensor:
         return torch.empty((self.workspace_bytes(),), dtype=torch.uint8, device=device)
@@ -119,18 +119,10 @@ class PromptAttention:
             raise ValueError("packed sequences need their offsets")
         return dev
 
-    def _memory(self, workspace, need, dev, stream):
-        if workspace is None and need:
-            with _allocate_on(stream):
-                workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-        if need and (workspace.device != dev or not workspace.is_contiguous()):
-            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-        return (workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()) if need else (None, None, 0)
-
     def __call__(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, extents: torch.Tensor | None = None, out=None,
-                 workspace: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
+                 stream: torch.cuda.Stream | None = None):
         if out is None and stream is None and self._forward is not None and (extents is not None or not self.sequences):
-            r = self._call(self._forward, q, k, v, extents, workspace)
+            r = self._call(self._forward, q, k, v, extents, None)
             if type(r) is tuple:
                 return r
             if r is not None:
@@ -144,11 +136,10 @@ class PromptAttention:
         self._check("o", o, self._o_shape, dev)
         if lse is not None:
             self._check("lse", lse, self._lse_shape, dev, torch.float32)
-        keep, at, size = self._memory(workspace, self._run_bytes, dev, stream)
         st = stream if stream is not None else torch.cuda.current_stream(dev)
         rc = self._lib.prompt_attention_run(self._h, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                             None if extents is None else extents.data_ptr(), o.data_ptr(),
-                                            None if lse is None else lse.data_ptr(), at, size, st.cuda_stream)
+                                            None if lse is None else lse.data_ptr(), st.cuda_stream)
         if rc != OK:
             raise FusedProjError(rc, "prompt_attention_run")
         return o, lse
@@ -167,17 +158,20 @@ class PromptAttention:
         self._check("o", o, self._o_shape, dev)
         self._check("lse", lse, self._lse_shape, dev, torch.float32)
         self._check("do", do, self._o_shape, dev)
-        if out is None:
-            with _allocate_on(stream):
+        with _allocate_on(stream):
+            if out is None:
                 out = tuple(torch.empty(s, dtype=torch.bfloat16, device=dev) for s in self._shapes)
+            if workspace is None:
+                workspace = torch.empty((self._workspace_bytes,), dtype=torch.uint8, device=dev)
         for name, t, shape in zip(("dq", "dk", "dv"), out, self._shapes):
             self._check(name, t, shape, dev)
-        keep, at, size = self._memory(workspace, self._backward_bytes, dev, stream)
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
         st = stream if stream is not None else torch.cuda.current_stream(dev)
         rc = self._lib.prompt_attention_backward(self._h, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                                  None if extents is None else extents.data_ptr(), o.data_ptr(),
-                                                 lse.data_ptr(), do.data_ptr(), *(t.data_ptr() for t in out), at, size,
-                                                 st.cuda_stream)
+                                                 lse.data_ptr(), do.data_ptr(), *(t.data_ptr() for t in out), workspace.data_ptr(),
+                                                 workspace.numel() * workspace.element_size(), st.cuda_stream)
         if rc != OK:
             raise FusedProjError(rc, "prompt_attention_backward")
         return tuple(out)

@@ -78,27 +78,25 @@ int prompt_attention_validate(const prompt_attention_desc *desc);
  * FUSED_PROJ_EINVAL for out == NULL, FUSED_PROJ_EHIP. */
 int prompt_attention_create(const prompt_attention_desc *desc, prompt_attention_t *out);
 
-/* Bytes of device workspace prompt_attention_run and prompt_attention_backward need (perhaps 0).
- * One workspace serves both; its contents do not matter, and calls that share it must not
- * overlap in time. */
-int prompt_attention_workspace_size(prompt_attention_t plan, size_t *run, size_t *backward);
-
 /* Enqueues the forward pass on `stream` (a hipStream_t; NULL = the legacy default stream) and
  * returns; allocates nothing, never synchronises.
  *   q, k, v   device, laid out as the descriptor says, 16-byte aligned
  *   extents   device int32 [b] or [sequences + 1]; may be NULL where sequences is 0
  *   o         device [b, T, H*hd] (token-major: what a projection of it reads), 16-byte aligned
  *   lse       device fp32 [b*H, T] (natural logarithms); NULL where no backward pass wants it
- *   workspace device, at least the size above, 16-byte aligned
- * Errors: FUSED_PROJ_EINVAL (a NULL pointer, a short workspace, another device current),
- * FUSED_PROJ_EALIGN, FUSED_PROJ_EALIAS (an output overlapping another or an input),
- * FUSED_PROJ_EHIP. */
+ * Errors: FUSED_PROJ_EINVAL (a NULL pointer, another device current), FUSED_PROJ_EALIGN,
+ * FUSED_PROJ_EALIAS (an output overlapping another or an input), FUSED_PROJ_EHIP. */
 int prompt_attention_run(prompt_attention_t plan, const void *q, const void *k, const void *v, const int32_t *extents,
-                         void *o, void *lse, void *workspace, size_t workspace_bytes, void *stream);
+                         void *o, void *lse, void *stream);
+
+/* Bytes of device workspace prompt_attention_backward needs (0 when there are no tokens). */
+int prompt_attention_backward_workspace_size(prompt_attention_t plan, size_t *bytes);
 
 /* Enqueues the backward pass. q, k, v, extents: the forward pass's; o, lse: its outputs; d_o: the
  * upstream gradient [b, T, H*hd]; dq [b, H, T, hd], dk and dv [b, KVH, T, hd]: head-major and
- * dense whatever the inputs' strides. Errors as prompt_attention_run. */
+ * dense whatever the inputs' strides. workspace: device, at least the size above, 16-byte
+ * aligned; its contents do not matter, and calls that share it must not overlap in time.
+ * Errors as prompt_attention_run; a short workspace is FUSED_PROJ_EINVAL. */
 int prompt_attention_backward(prompt_attention_t plan, const void *q, const void *k, const void *v,
                               const int32_t *extents, const void *o, const void *lse, const void *d_o, void *dq,
                               void *dk, void *dv, void *workspace, size_t workspace_bytes, void *stream);

@@ -46,8 +46,7 @@ class Case:
         plan = self.plan(q, k, v)
         nan = lambda s, dtype=BF16: torch.full(s, float("nan"), dtype=dtype, device=DEV)
         ws = torch.full((plan.workspace_bytes() // 4 + 4,), float("nan"), device=DEV)
-        o, lse = plan(q, k, v, e, out=(nan((self.b, self.t, self.h * self.hd)), nan((self.b * self.h, self.t), torch.float32)), workspace=ws)
-        ws.fill_(float("nan"))
+        o, lse = plan(q, k, v, e, out=(nan((self.b, self.t, self.h * self.hd)), nan((self.b * self.h, self.t), torch.float32)))
         grads = plan.backward(q, k, v, o, lse, do, e, out=tuple(nan(x.shape) for x in (q, k, v)), workspace=ws)
         torch.cuda.synchronize()
         got = {"o": o.view(self.b, self.t, self.h, self.hd), "lse": lse.view(self.b, self.h, self.t)}
@@ -99,6 +98,9 @@ CASES += [
     *(dict(batch=2, tokens=150, heads=128, kvh=64, hd=hd, causal=c, extents=[150, 97]) for hd, c in ((16, True), (64, False), (72, True), (128, False), (120, True))),
     dict(batch=1, tokens=515, heads=128, kvh=128, hd=64, sequences=5, extents=[2, 60, 260, 261, 400, 513]),
     dict(batch=1, tokens=515, heads=128, kvh=64, hd=128, sequences=5, extents=[2, 60, 260, 261, 400, 513], causal=False),
+    # a group's heads in parts (few keys), also of an odd number of heads
+    dict(batch=1, tokens=300, heads=15, kvh=3, hd=64, sequences=2, extents=[3, 130, 290]), dict(batch=1, tokens=260, heads=8, kvh=1, hd=128, causal=False),
+    dict(batch=1, tokens=300, heads=6, kvh=2, hd=200), dict(batch=2, tokens=257, heads=5, kvh=1, hd=256, extents=[257, 100], layout="qkv"),
     # steep and flat
     dict(batch=1, tokens=150, heads=2, kvh=2, hd=64, scale=3.0), dict(batch=1, tokens=150, heads=2, kvh=2, hd=64, scale=1e-6),
 ]
@@ -267,7 +269,7 @@ def test_refusals():
     ws = plan.alloc_workspace(DEV)
     lib, h, p = plan._lib, plan._h, lambda t: None if t is None else t.data_ptr()
     st = torch.cuda.current_stream().cuda_stream
-    run = lambda q=q, k=k, v=v, e=e, o=o, lse=lse, more=0: lib.prompt_attention_run(h, p(q), p(k), p(v), p(e), p(o) + more if o is not None else None, p(lse), p(ws), ws.numel(), st)
+    run = lambda q=q, k=k, v=v, e=e, o=o, lse=lse, more=0: lib.prompt_attention_run(h, p(q), p(k), p(v), p(e), p(o) + more if o is not None else None, p(lse), st)
     assert run(q=None) == EINVAL and run(e=None) == EINVAL and run(o=None) == EINVAL
     assert run(more=2) == EALIGN and run(k=k.flatten()[1:]) == EALIGN
     assert run(o=q) == EALIAS and run(o=v) == EALIAS and run(lse=o) == EALIAS and run(lse=e) == EALIAS

@@ -71,8 +71,8 @@ def test_wrong_enums_and_null():
     assert lib.prompt_attention_create(ctypes.byref(_desc()), None) == fpa.EINVAL
     assert lib.prompt_attention_destroy(None) == fpa.OK
     n = ctypes.c_size_t()
-    assert lib.prompt_attention_workspace_size(None, ctypes.byref(n), ctypes.byref(n)) == fpa.EINVAL
-    assert lib.prompt_attention_run(*[None] * 8, 0, None) == fpa.EINVAL
+    assert lib.prompt_attention_backward_workspace_size(None, ctypes.byref(n)) == fpa.EINVAL
+    assert lib.prompt_attention_run(*[None] * 8) == fpa.EINVAL
     assert lib.prompt_attention_backward(*[None] * 12, 0, None) == fpa.EINVAL
 
 
