@@ -27,7 +27,10 @@ namespace {
 
 using namespace fp::dev;
 
-constexpr int kHeads = 4;   // heads of a thread
+// Heads of a thread: 4 share their sines and cosines (2: 2 x 4096 x 96 heads of 128 no faster, 8: a tenth slower), 1 where
+// workgroups of 4 would not fill the card (2 x 1024 x 24 heads of 32: 5.7 -> 4.9 us).
+constexpr int kHeads = 4;
+constexpr int64_t kFewBlocks = 512;
 constexpr int64_t kMostDims = 4096;
 constexpr long double kTwoPi = 6.283185307179586476925286766559005768L;
 // Angles are extended-precision numbers, off by 2^-63 of themselves: up to this many radians a
@@ -96,9 +99,18 @@ struct alignas(sizeof(T) * N) Unit {
     T x[N];
 };
 
+// Past the caches: nothing is read again here (2 x 4096 x 96 heads of 128: 94 -> 82 us).
+template <typename T, int N>
+__device__ __forceinline__ void store_unit(T* p, const Unit<T, N>& u) {
+    if constexpr (sizeof(u) == 16)
+        __builtin_nontemporal_store(__builtin_bit_cast(u32x4, u), reinterpret_cast<u32x4*>(p));
+    else
+        *reinterpret_cast<Unit<T, N>*>(p) = u;
+}
+
 // HALF: a unit is W pairs, elements i .. i + W - 1 and i + rd/2 ..; behind the rotated width W
 // elements that are copied. Otherwise it is W consecutive elements, pairs inside.
-template <typename T, int W, bool HALF>
+template <typename T, int W, bool HALF, int G>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
     const uint32_t item = blockIdx.x * 256u + threadIdx.x;
     if (item >= a.items) return;
@@ -111,11 +123,11 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
     // HALF: a unit is rotated or copied whole (W divides half); interleaved: pair by pair
     const bool turns = pair0 < half;
     const int at = HALF && !turns ? a.rd + (pair0 - half) : HALF ? pair0 : pair0 * 2;
-    const int head0 = blockIdx.y * kHeads;
+    const int head0 = blockIdx.y * G;
 
-    Unit<T, W> x[kHeads], y[kHeads];
+    Unit<T, W> x[G], y[G];
 #pragma unroll
-    for (int g = 0; g < kHeads; ++g)
+    for (int g = 0; g < G; ++g)
         if (head0 + g < a.heads) {
             const T* p = reinterpret_cast<const T*>(row_of(a.from, a, head0 + g, bi, t, sizeof(T))) + at;
             x[g] = *reinterpret_cast<const Unit<T, W>*>(p);
@@ -133,7 +145,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
         }
     }
 #pragma unroll
-    for (int g = 0; g < kHeads; ++g) {
+    for (int g = 0; g < G; ++g) {
         if (head0 + g >= a.heads) break;
         T* p = reinterpret_cast<T*>(row_of(a.to, a, head0 + g, bi, t, sizeof(T))) + at;
         const bool rotate = turns && head0 + g < a.H + a.KVH;
@@ -149,8 +161,8 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
                 }
             }
         }
-        *reinterpret_cast<Unit<T, W>*>(p) = x[g];
-        if (HALF && turns) *reinterpret_cast<Unit<T, W>*>(p + half) = y[g];
+        store_unit(p, x[g]);
+        if (HALF && turns) store_unit(p + half, y[g]);
     }
 }
 
@@ -247,12 +259,20 @@ void pair_turns(const rope_desc& d, int64_t rd, uint64_t (&f)[kMostDims / 2]) {
 }
 
 // W: of a half's units; interleaved rows are taken in pieces of 16 bytes.
-template <typename T, int W>
-void launch(const RopeArgs& a, bool half, dim3 grid, hipStream_t st) {
+template <typename T, int W, int G>
+void launch_heads(const RopeArgs& a, bool half, hipStream_t st) {
+    const dim3 grid((unsigned)(((int64_t)a.items + 255) / 256), (unsigned)((a.heads + G - 1) / G));
     if (half)
-        hipLaunchKernelGGL((rope_kernel<T, W, true>), grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((rope_kernel<T, W, true, G>), grid, dim3(256), 0, st, a);
     else
-        hipLaunchKernelGGL((rope_kernel<T, (sizeof(T) == 2 ? 8 : 4), false>), grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((rope_kernel<T, (sizeof(T) == 2 ? 8 : 4), false, G>), grid, dim3(256), 0, st, a);
+}
+template <typename T, int W>
+void launch(const RopeArgs& a, bool half, hipStream_t st) {
+    if (((int64_t)a.items + 255) / 256 * ((a.heads + kHeads - 1) / kHeads) < kFewBlocks)
+        launch_heads<T, W, 1>(a, half, st);
+    else
+        launch_heads<T, W, kHeads>(a, half, st);
 }
 
 int run(rope_t h, const Side& from, const Side& to, const int32_t* positions, bool with_v, bool backward, void* stream) {
@@ -307,21 +327,20 @@ int run(rope_t h, const Side& from, const Side& to, const int32_t* positions, bo
     a.magnitude = d.magnitude == 0.0 ? 1.0f : (float)d.magnitude;
     a.div_units = fp::make_fastdiv_u31((uint32_t)a.units);
     a.div_t = fp::make_fastdiv_u31((uint32_t)a.T);
-    const dim3 grid((unsigned)(((int64_t)a.items + 255) / 256), (unsigned)((a.heads + kHeads - 1) / kHeads));
     const bool half = d.pairs == ROPE_PAIRS_HALF;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     if (d.dtype == FUSED_PROJ_BF16) {
         switch (h->r.width) {
-            case 8: launch<__bf16, 8>(a, half, grid, st); break;
-            case 4: launch<__bf16, 4>(a, half, grid, st); break;
-            case 2: launch<__bf16, 2>(a, half, grid, st); break;
-            default: launch<__bf16, 1>(a, half, grid, st);
+            case 8: launch<__bf16, 8>(a, half, st); break;
+            case 4: launch<__bf16, 4>(a, half, st); break;
+            case 2: launch<__bf16, 2>(a, half, st); break;
+            default: launch<__bf16, 1>(a, half, st);
         }
     } else {
         switch (h->r.width) {
-            case 4: launch<float, 4>(a, half, grid, st); break;
-            case 2: launch<float, 2>(a, half, grid, st); break;
-            default: launch<float, 1>(a, half, grid, st);
+            case 4: launch<float, 4>(a, half, st); break;
+            case 2: launch<float, 2>(a, half, st); break;
+            default: launch<float, 1>(a, half, st);
         }
     }
     return hip_status(hipGetLastError());
