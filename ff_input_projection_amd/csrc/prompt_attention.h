@@ -333,13 +333,23 @@ __device__ __forceinline__ void product(f32x16 (&x)[NB], const B& b, unsigned ba
     }
 }
 
+// What that rounding leaves, rounded: the two together have 16 bits of X.
+template <int NB>
+__device__ __forceinline__ void rest_to_operands(bf16x8 (&o)[2 * NB], const bf16x8 (&first)[2 * NB], const f32x16 (&x)[NB]) {
+#pragma unroll
+    for (int s = 0; s < 2 * NB; ++s)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[s][i] = (__bf16)(x[s >> 1][8 * (s & 1) + i] - (float)first[s][i]);
+}
+
 // Y^T += A'^T X for the tile of 32 NB rows whose turned base is given; C tiles of Y^T a group. PARTS: the wave has every
-// PARTS-th tile (32 elements of the heads) of Y^T alone, the first as turned_base says.
+// PARTS-th tile (32 elements of the heads) of Y^T alone, the first as turned_base says. rest: of X, the same way.
 // Where the mask hides some of the tile's rows from some of the wave's (`edge`), their values in X
 // are 0, but 0 times an infinity or NaN is NaN. A product of the tile with zeros tells whether it
 // holds any; then they are left out here, and true is returned: add_left_out has to follow.
 template <int D, int NB, int C, int PARTS = 1>
-__device__ __forceinline__ bool add_turned(f32x16 (&y)[D / 32 / PARTS], const bf16x8 (&x)[2 * NB], unsigned base, bool edge) {
+__device__ __forceinline__ bool add_turned(f32x16 (&y)[D / 32 / PARTS], const bf16x8 (&x)[2 * NB], unsigned base, bool edge,
+                                           const bf16x8* rest = nullptr) {
     using R = Rows<D>;
     constexpr int T = D / 32 / PARTS, S = 2 * NB, P = T / C;   // P groups a step
     static_assert(P * C == T, "whole groups");
@@ -374,6 +384,11 @@ __device__ __forceinline__ bool add_turned(f32x16 (&y)[D / 32 / PARTS], const bf
 #pragma unroll
         for (int c = 0; c < C; ++c)
             y[i % P * C + c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i & 1][c], x[i / P], y[i % P * C + c], 0, 0, 0);
+        if (rest) {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                y[i % P * C + c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i & 1][c], rest[i / P], y[i % P * C + c], 0, 0, 0);
+        }
         __builtin_amdgcn_sched_barrier(0);
     }
     return !all_finite;

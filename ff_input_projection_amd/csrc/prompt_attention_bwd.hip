@@ -102,7 +102,9 @@ __global__ __launch_bounds__(64 * RW * H, RW * H == 4 && D <= 128 ? 2 : 1) void 
         }
         bf16x8 w[2];
         to_operands<1>(w, x);
-        left_out |= add_turned<D, 1, D / 32>(dq, w, kt + turned, edge);
+        bf16x8 rest[2];
+        rest_to_operands<1>(rest, w, x);
+        left_out |= add_turned<D, 1, D / 32>(dq, w, kt + turned, edge, rest);
     };
 
     if constexpr (PADDED) __syncthreads();
@@ -210,7 +212,7 @@ __global__ __launch_bounds__(64 * RW * H * PARTS, RW * H * PARTS == 4 && D <= 96
         const bool edge = at_edge(p);
         f32x16 x[1], y[1];
         constexpr int C = T == 4 && D >= 128 ? 2 : T, J = D >= 128 ? 1 : 2;
-        bf16x8 w[2], dw[2];
+        bf16x8 w[2], dw[2], rest[2];
         {
             const int h = lane >> 5;
             product<D, 1, J>(
@@ -238,11 +240,12 @@ __global__ __launch_bounds__(64 * RW * H * PARTS, RW * H * PARTS == 4 && D <= 96
             }
             to_operands<1>(w, x);
             to_operands<1>(dw, y);
+            rest_to_operands<1>(rest, dw, y);
             __builtin_amdgcn_sched_barrier(0);
         }
         left_out |= add_turned<D, 1, C, PARTS>(dv, w, dt + turned, edge);
         // where a token's q is not finite neither is its lse, so that ds is NaN for every key that it sees
-        add_turned<D, 1, C, PARTS>(dk, dw, qt + turned, edge);
+        add_turned<D, 1, C, PARTS>(dk, dw, qt + turned, edge, rest);
     };
 
     if constexpr (PADDED) __syncthreads();

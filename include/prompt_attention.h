@@ -30,8 +30,8 @@
  * lse, and nothing of theirs reaches another token.
  *
  * Numerics. Products of bf16 numbers are exact, their sums, the softmax and its statistics fp32; the
- * probabilities, and ds in the backward pass, are rounded to bf16 for their products with v, do, k
- * and q; each output is rounded once. Logits are fp32: x_ij log2(e) stays below 2^127. A NaN or an
+ * probabilities are rounded to bf16 for their products with v and do, ds to the sum of two bf16
+ * numbers for those with k and q; each output is rounded once. Logits are fp32: x_ij log2(e) stays below 2^127. A NaN or an
  * infinity reaches the tokens that the formulas lead it to, and no token that does not see it.
  * Results do not depend on timing: no atomics in global memory.
  *
