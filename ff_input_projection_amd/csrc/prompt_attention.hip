@@ -1,11 +1,21 @@
 // Attention over whole prompts (gfx950): the forward pass, and the C ABI
 // (include/prompt_attention.h; tiles and operand layouts: prompt_attention.h beside this file).
 //
-// A workgroup of 4 waves takes 128 tokens of a query head, 32 a wave, and passes over the keys
-// that any of them sees in tiles of 64 (32 for heads above 128). X = K Q^T, so a lane has half of
-// a tile's logits of one token; the running maximum moves only when a logit passes it by 2^8
-// (probabilities in bf16 keep their relative precision), so that between moves lanes exchange
-// nothing. Masks are taken only in tiles where some token of the wave does not see some key.
+// A wave takes 32 tokens of a query head and passes over the keys that any of its workgroup's
+// tokens sees. X = K Q^T, so a lane has half of a tile's logits of one token; the running maximum
+// moves only when a logit passes it by 2^8 (probabilities in bf16 keep their relative precision),
+// so that between moves lanes exchange nothing. Masks are taken only in tiles where some token
+// of the wave does not see some key.
+//
+// A workgroup is 4 waves of different tokens and tiles of 64 keys, two workgroups a CU, so that one wave's
+// products overlap the other's softmax; with few workgroups 2 rows of 4 waves that share the
+// tokens and take 32 keys of 128 each (few_workgroups has both sides' times); above heads of 128 the
+// registers hold one wave a SIMD and tiles of 32. k and v come by direct-to-LDS loads, two tiles each.
+//
+// Measured: 8192 tokens, 32 heads on 8 of 128, causal, 555 us: 990 TFLOP/s, 0.8 of a large
+// library product's rate. Bound by both units of a SIMD: matrix units busy 4/10 of the time, vector
+// units half. Without the softmax's operations it takes 504 us, without the second product 408, on zeros 473 (the clock:
+// power).
 #include <cmath>
 #include <cstring>
 #include <new>
@@ -246,7 +256,8 @@ int check(const prompt_attention_desc* d, fp::AttentionPlan* out, int64_t* kvh_o
     const int64_t lim = (int64_t(1) << 31) - 1, kvh = d->n_kv_heads > 0 ? d->n_kv_heads : d->n_heads;
     if (d->tokens >= (1 << 30) || d->sequences >= (1 << 30) || d->batch > lim || d->n_heads > lim) return FUSED_PROJ_EUNSUPPORTED;
     if (d->batch * d->n_heads > lim / d->tokens) return FUSED_PROJ_EUNSUPPORTED;
-    if (d->batch * d->n_heads > lim / ((d->tokens + 31) / 32)) return FUSED_PROJ_EUNSUPPORTED;
+    // a launch has below 2^32 threads, and none more than 512 for 64 tokens of a head
+    if (d->batch * d->n_heads >= (int64_t(1) << 23) / ((d->tokens + 63) / 64)) return FUSED_PROJ_EUNSUPPORTED;
     for (const int64_t* s : {d->q_strides, d->k_strides, d->v_strides}) {
         for (int i = 0; i < 3; ++i)
             if (s[i] % 8 != 0) return FUSED_PROJ_EUNSUPPORTED;

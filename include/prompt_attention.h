@@ -70,8 +70,8 @@ typedef struct prompt_attention_plan *prompt_attention_t;
 /* Host-only check. FUSED_PROJ_OK, FUSED_PROJ_EINVAL (malformed: sizes, flags, KVH not dividing H,
  * strides below 0, packed sequences with another batch than 1, sm_scale outside its range) or
  * FUSED_PROJ_EUNSUPPORTED: not bf16, hd no multiple of 8 or above 256, strides no multiples
- * of 8, a token stride above 2^24, T of 2^30 or more, sequences of 2^30 or more, b T H or
- * b H ceil(T / 32) of 2^31 or more, or an address beyond 2^60. */
+ * of 8, a token stride above 2^24, T of 2^30 or more, sequences of 2^30 or more, b T H of
+ * 2^31 or more, b H at or above 2^23 / ceil(T / 64) rounded down, or an address beyond 2^60. */
 int prompt_attention_validate(const prompt_attention_desc *desc);
 
 /* Validates and fixes the split of the work; touches no GPU memory. Errors: as validate,

@@ -56,6 +56,9 @@ def _desc(batch=2, tokens=5, n_heads=8, head_dim=64, **kw):
     (dict(k_strides=(1 << 60, 8, 8)), fpa.EUNSUPPORTED), (dict(tokens=1 << 30), fpa.EUNSUPPORTED),
     (dict(batch=1, sequences=1 << 30), fpa.EUNSUPPORTED), (dict(batch=1 << 20, tokens=1 << 12), fpa.EUNSUPPORTED),
     (dict(n_heads=1 << 40), fpa.EUNSUPPORTED), (dict(n_heads=1 << 19), fpa.EUNSUPPORTED), (dict(n_heads=1 << 18), fpa.OK),
+    # launches of 2^32 threads
+    (dict(batch=1 << 20, tokens=1), fpa.EUNSUPPORTED), (dict(batch=(1 << 20) - 1, tokens=1), fpa.OK),
+    (dict(batch=1 << 18, tokens=200), fpa.EUNSUPPORTED), (dict(batch=(1 << 18) - 1, tokens=200), fpa.OK),
 ])
 def test_validate(kw, code):
     assert validate_prompt_attention(_desc(**kw)) == code
