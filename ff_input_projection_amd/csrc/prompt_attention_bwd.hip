@@ -14,7 +14,6 @@ namespace {
 using namespace fp::dev;
 using fp::AttentionArgs;
 
-
 // Shapes of a workgroup: RW rows of waves with 32 tokens each, and H waves a row that share them and take S
 // times 32 keys in turn of each tile of 32 H S; their sums are added at the end.
 template <int D, bool PADDED, int RW, int H, int S>
@@ -317,7 +316,8 @@ __global__ __launch_bounds__(64 * RW * H * PARTS, RW * H * PARTS == 4 && D <= 96
 //   4 x 512 tokens, 12 heads (192 workgroups)    - / 36 / 41        8 x 512, 12 heads (384)  46 / 52 / -
 //   16 x 2048 (256)     108 / 94 / 100           causal             108 / 78 / 66
 //   32 x 2048 (512)     147 / 157 / 174          causal             133 / 136 / 129       16 x 4096, causal  236 / 194 / 205
-// Heads of 128 have registers for one wave a SIMD of 4 rows of one, and take two.
+// (All with ds in one bf16 number; 2 x 4096 tokens, 32 heads on 8 of 128, causal, take a seventh longer with two.) Heads of 128 have registers for one wave a SIMD
+// of 4 rows of one, and take two.
 int64_t few_key_blocks(const prompt_attention_desc& d) { return d.tokens < 1024 ? 160 : d.causal ? 512 : 256; }
 
 // Adds up the parts of dk and dv, 4 elements a thread.

