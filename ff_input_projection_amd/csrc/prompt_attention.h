@@ -57,6 +57,14 @@ inline bool few_workgroups(int64_t blocks, const prompt_attention_desc& d) {
     return d.tokens > 128 && (blocks < 256 || (d.tokens >= 1024 && blocks < (d.causal && d.head_dim <= 64 ? 768 : 512)));
 }
 
+// Sequences of up to 64 tokens: workgroups with a row of waves for every 32 that there are, and none idle. Forward and
+// backward, us, 128 tokens a workgroup / these: 512 x 32 tokens, 32 heads on 8 of 128, causal, 157, 395 / 95, 247; 512 x 17, 12
+// of 64, 24, 72 / 15, 36; 256 x 64, 32 on 8 of 128, 98, 279 / 85, 262. One sequence of 64 has no gain (backward 25 / 32).
+inline int short_rows(const prompt_attention_desc& d) {   // 0: the sequences are not short
+    if (d.tokens <= 32) return 1;
+    return d.tokens <= 64 && d.batch * d.n_heads >= 512 ? 2 : 0;
+}
+
 // Sets kv_parts.
 void plan_attention_backward(const prompt_attention_desc& d, int64_t kvh, AttentionPlan* p);
 hipError_t launch_attention(const prompt_attention_desc& d, const AttentionPlan& p, AttentionArgs a, hipStream_t st);
@@ -248,8 +256,9 @@ struct TileLoads {
         }
     }
 };
-// All outstanding loads of this wave have landed.
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// All outstanding loads of this wave have landed, and its reads of LDS are done (a workgroup of one wave has no
+// barrier that waits for them).
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
 
 // 32 rows of a wave as operand B of X: row lane % 32 of `src` rows (64-bit address of the lane's
 // row), elements 16 kk + 8 (lane / 32) .. + 7; zeros behind hd and for rows that are not there.

@@ -10,7 +10,7 @@
 // A workgroup is 4 waves of different tokens and tiles of 64 keys, two workgroups a CU, so that one wave's
 // products overlap the other's softmax; with few workgroups 2 rows of 4 waves that share the
 // tokens and take 32 keys of 128 each (few_workgroups has both sides' times); above heads of 128 the
-// registers hold one wave a SIMD and tiles of 32. k and v come by direct-to-LDS loads, two tiles each.
+// registers hold one wave a SIMD and tiles of 32. Short sequences have workgroups without idle waves (short_rows). k and v come by direct-to-LDS loads, two tiles each.
 //
 // Measured: 8192 tokens, 32 heads on 8 of 128, causal, 555 us: 990 TFLOP/s, 0.8 of a large
 // library product's rate. Bound by both units of a SIMD: matrix units busy 4/10 of the time, vector
@@ -44,7 +44,7 @@ __device__ __forceinline__ Place place_of(const AttentionArgs& a) {
 // Shapes of a workgroup: RW rows of waves with 32 tokens each, and H waves a row that share them and take
 // 32 NB keys in turn of each tile of 32 NB H; what they have is joined at the end.
 template <int D, bool PADDED, int RW, int H, int NB>
-__global__ __launch_bounds__(64 * RW * H, RW * H == 4 && D <= 128 ? 2 : 1) void attention_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(64 * RW * H, RW * H <= 4 && D <= 128 ? 2 : 1) void attention_kernel(AttentionArgs a) {
     using R = Rows<D>;
     constexpr int NW = RW * H, BM = 32 * RW, BW = 32 * NB, BN = BW * H, TILE = BN * R::BYTES;
     __shared__ __attribute__((aligned(1024))) unsigned char tiles[4 * TILE];   // k, k, v, v
@@ -192,7 +192,12 @@ template <int D>
 void launch(const prompt_attention_desc& d, const AttentionArgs& a, hipStream_t st) {
     // workgroups of 128 tokens
     const int64_t blocks = d.batch * d.n_heads * ((d.tokens + 127) / 128);
-    if constexpr (D > 128)
+    const int rows = fp::short_rows(d);
+    if (rows == 1)
+        launch_shape<D, 1, 1, 1>(d, a, st);
+    else if (rows == 2)
+        launch_shape<D, 2, 1, 1>(d, a, st);
+    else if constexpr (D > 128)
         launch_shape<D, 4, 1, 1>(d, a, st);
     else if (fp::few_workgroups(blocks, d))
         launch_shape<D, 2, 4, 1>(d, a, st);

@@ -17,7 +17,7 @@ using fp::AttentionArgs;
 // Shapes of a workgroup: RW rows of waves with 32 tokens each, and H waves a row that share them and take S
 // times 32 keys in turn of each tile of 32 H S; their sums are added at the end.
 template <int D, bool PADDED, int RW, int H, int S>
-__global__ __launch_bounds__(64 * RW * H, RW * H == 4 && D <= 128 ? 2 : 1) void attention_dq_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(64 * RW * H, RW * H <= 4 && D <= 128 ? 2 : 1) void attention_dq_kernel(AttentionArgs a) {
     using R = Rows<D>;
     constexpr int NW = RW * H, BM = 32 * RW, BN = 32 * H * S, TILE = BN * R::BYTES;
     __shared__ __attribute__((aligned(1024))) unsigned char tiles[4 * TILE];   // k, k, v, v
@@ -142,7 +142,7 @@ __global__ __launch_bounds__(64 * RW * H, RW * H == 4 && D <= 128 ? 2 : 1) void 
 // waves have the same keys and tokens, and every other 32 elements of dk and dv (PARTS); both
 // compute P and ds. One wave with all of them has no registers for a second on its SIMD, and at 256 not for itself.
 template <int D, bool PADDED, int RW, int H, int S, int PARTS>
-__global__ __launch_bounds__(64 * RW * H * PARTS, RW * H * PARTS == 4 && D <= 96 ? 2 : 1) void attention_dkv_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(64 * RW * H * PARTS, RW * H * PARTS <= 4 && D <= 96 ? 2 : 1) void attention_dkv_kernel(AttentionArgs a) {
     using R = Rows<D>;
     // Heads of 128 and more: the accumulators, k and v leave no registers for two waves a SIMD (heads above 128: for one), so v's rows
     // stay in LDS.
@@ -360,6 +360,17 @@ void launch_dq(const prompt_attention_desc& d, AttentionArgs a, hipStream_t st) 
 
 template <int D>
 void launch(const prompt_attention_desc& d, const fp::AttentionPlan& p, AttentionArgs a, hipStream_t st) {
+    const int rows = fp::short_rows(d);
+    if (rows == 1) {
+        launch_dq<D, 1, 1, 1>(d, a, st);
+        launch_dkv<D, 1, 1, 1, D <= 128 ? 1 : 2>(d, p, a, st);
+        return;
+    }
+    if (rows == 2) {
+        launch_dq<D, 2, 1, 1>(d, a, st);
+        launch_dkv<D, 2, 1, 1, D <= 128 ? 1 : 2>(d, p, a, st);
+        return;
+    }
     // workgroups of 128 tokens
     const int64_t blocks = d.batch * d.n_heads * ((d.tokens + 127) / 128);
     if constexpr (D > 128)

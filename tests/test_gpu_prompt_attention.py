@@ -385,3 +385,31 @@ def test_a_prompt_then_single_tokens():
     prompt.write(storage, k, v, table, n)
     last = step.attend(storage, q[:, -1:].contiguous(), table, n)
     assert (last[:, 0].float() - whole[:, -1].float()).abs().max() <= 0.05
+
+
+SHORT = [dict(batch=7, tokens=t, heads=4, kvh=2, hd=hd, causal=c) for t, hd, c in
+         ((1, 128, True), (2, 256, False), (17, 8, True), (17, 64, False), (31, 96, True), (32, 32, False), (32, 128, True), (29, 136, True),
+          (32, 192, False), (30, 256, True))]
+SHORT += [dict(batch=4, tokens=t, heads=128, kvh=64, hd=hd, causal=c) for t, hd, c in
+          ((33, 64, True), (50, 32, False), (64, 128, True), (64, 64, False), (49, 80, True), (40, 96, False), (57, 104, True), (36, 192, True),
+           (64, 200, False), (63, 256, True))]
+SHORT += [
+    dict(batch=5, tokens=30, heads=4, kvh=1, hd=64, extents=[0, 1, 30, 99, -2], causal=False),
+    dict(batch=4, tokens=60, heads=128, kvh=128, hd=128, extents=[0, 33, 60, 7], layout="qkv"),
+    dict(batch=1, tokens=31, heads=6, kvh=3, hd=128, sequences=5, extents=[2, 2, 9, 10, 25, 30]),
+    dict(batch=1, tokens=61, heads=512, kvh=256, hd=64, sequences=4, extents=[1, 20, 20, 47, 60], causal=False),
+]
+
+
+@pytest.mark.parametrize("kw", SHORT, ids=["_".join(str(x) if not isinstance(x, list) else f"e{sum(x) % 1000}" for x in c.values()) for c in SHORT])
+def test_short_sequences(kw):
+    print(f"[case] attention {kw}", flush=True)
+    c = Case(**kw)
+    check(c.run(), c.want())
+
+
+@pytest.mark.parametrize("kw", [dict(batch=1, tokens=64, heads=512, kvh=256, hd=128, extents=[61]), dict(batch=3, tokens=32, heads=2, kvh=1, hd=64),
+                                dict(batch=1, tokens=60, heads=512, kvh=512, hd=64, sequences=2, extents=[0, 32, 58], causal=False)])
+@pytest.mark.parametrize("which", ["v", "k", "q", "do"])
+def test_short_sequences_that_are_not_finite(kw, which):
+    test_what_is_not_finite_reaches_those_that_see_it(kw, which)
