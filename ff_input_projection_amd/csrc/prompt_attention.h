@@ -504,5 +504,18 @@ __device__ __forceinline__ WaveSight wave_sight(Span s) {
     return w;
 }
 
+// From the least first to the greatest last row of NW waves' spans (each the same in all lanes of its wave).
+template <int NW>
+__device__ __forceinline__ Span of_workgroup(Span s) {
+    if constexpr (NW > 1) {
+        __shared__ Span spans[NW];
+        if ((threadIdx.x & 63) == 0) spans[threadIdx.x >> 6] = s;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NW; ++i) s = Span{min(s.first, spans[i].first), max(s.last, spans[i].last)};
+    }
+    return Span{__builtin_amdgcn_readfirstlane(s.first), __builtin_amdgcn_readfirstlane(s.last)};
+}
+
 }  // namespace dev
 }  // namespace fp

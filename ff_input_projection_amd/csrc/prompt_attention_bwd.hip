@@ -7,12 +7,25 @@
 // the group, and leaves dk and dv. 7 products of the forward pass's size where 5 would do in one
 // kernel: there dq would be summed by atomics, in an order that changes from run to run, or
 // through partial sums in memory.
+//
+// D_i is sum_j p_ij dp_ij. What the caller has of o is rounded to bf16, and ds = p (dp - D) is a difference: with D from that o
+// alone dq and dk were off by 0.0040 of their norm at 2 tokens and 0.0030 at 8 (heads of 128, causal, normal inputs), where
+// their own rounding is 0.0017. The ds of a row sum to 0 if D is right, so their sum is what D lacks, and the first kernel
+// leaves the second a D with that sum added. For dq itself it comes too late; rows that see few keys, where it matters most, get it
+// beforehand (kFewKeys).
 #include "prompt_attention.h"
 
 namespace {
 
 using namespace fp::dev;
 using fp::AttentionArgs;
+
+// Rows that see at most this many keys have their D corrected before dq is formed, by two products more for these keys. In other
+// rows what o's rounding leaves in dq falls with the root of the number of keys that their softmax spreads over: normal inputs,
+// 512 tokens, causal, dq is off by 0.0020 of its norm without any of it, by 0.0017 with; with logits three times as steep by
+// 0.0030 and 0.0025, and by 0.0017 if all rows were. The backward pass in us, none / these / all rows: 2 x 4096 tokens, 32 heads on 8 of 128,
+// causal, 1522 / 1526 / 1788; 32 x 512 ragged, 12 of 64, 145 / 145 / 164; 256 x 128, 32 on 8 of 128, 532 / 582 / 582; 512 x 7, 176 / 191 / 191.
+constexpr int kFewKeys = 128;
 
 // Shapes of a workgroup: RW rows of waves with 32 tokens each, and H waves a row that share them and take S
 // times 32 keys in turn of each tile of 32 H S; their sums are added at the end.
@@ -62,10 +75,10 @@ __global__ __launch_bounds__(64 * RW * H, RW * H <= 4 && D <= 128 ? 2 : 1) void 
     if (a.causal && there) mine.last = row;
     const WaveSight sight = wave_sight(mine);
     if (!there) lse = delta = 0.0f;
-    if (row < a.T && lane < 32 && turn == 0) {
-        a.stats[stat] = lse;
-        a.stats[(int64_t)a.H * a.T * a.batch + stat] = delta;
-    }
+    const bool is_few = there && mine.last - mine.first < kFewKeys;
+    const Span few = is_few ? mine : Span{kNone, kNone};
+    const WaveSight few_sight = wave_sight(few);
+    const Span few_keys = of_workgroup<NW>(few_sight.any ? Span{few_sight.low, few_sight.high} : Span{kNone, -1});
 
     f32x16 dq[D / 32];
 #pragma unroll
@@ -79,16 +92,13 @@ __global__ __launch_bounds__(64 * RW * H, RW * H <= 4 && D <= 128 ? 2 : 1) void 
     k_loads.init(a.k_st);
     v_loads.init(a.v_st);
     const unsigned plain = R::plain_base(), turned = R::turned_base();
-    const auto issue = [&](int p, int set) {
-        k_loads.issue(k + (int64_t)p * a.k_st, a.k_st, lds + set * TILE, high + 1 - p, a.hd);
-        v_loads.issue(v + (int64_t)p * a.v_st, a.v_st, lds + (2 + set) * TILE, high + 1 - p, a.hd);
+    const auto issue = [&](int p, int set, int last) __attribute__((always_inline)) {
+        k_loads.issue(k + (int64_t)p * a.k_st, a.k_st, lds + set * TILE, last + 1 - p, a.hd);
+        v_loads.issue(v + (int64_t)p * a.v_st, a.v_st, lds + (2 + set) * TILE, last + 1 - p, a.hd);
     };
-    bool left_out = false;
-    const auto at_edge = [&](int p) { return p < sight.full_from || p + 31 > sight.full_to; };
-    const auto mine_at_edge = [&](int p) { return (p - low) / 32 % H == turn && at_edge(p); };
-    const auto take = [&](int p, unsigned kt, unsigned vt) {
-        const bool edge = at_edge(p);
-        f32x16 x[1], y[1];
+    float missing = 0.0f;   // what D lacks: the sum of this lane's ds
+    const auto ds_of = [&](f32x16 (&x)[1], int p, unsigned kt, unsigned vt, Span span, bool edge) __attribute__((always_inline)) {
+        f32x16 y[1];
         product<D, 1, 2>(x, [&](int kk) { return q[kk]; }, kt + plain);
         product<D, 1, 2>(y, [&](int kk) { return d_o[kk]; }, vt + plain);
 #pragma unroll
@@ -97,8 +107,33 @@ __global__ __launch_bounds__(64 * RW * H, RW * H <= 4 && D <= 128 ? 2 : 1) void 
         if (edge) {
             asm volatile("");   // a branch, not selects
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[0][i] = sees(mine, p + value_row(i)) ? x[0][i] : 0.0f;
+            for (int i = 0; i < 16; ++i) x[0][i] = sees(span, p + value_row(i)) ? x[0][i] : 0.0f;
         }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) missing += x[0][i];
+    };
+    // `missing` of both halves of a row and of its H waves, in one order. Between two calls lies a barrier of the loop over the tiles.
+    __shared__ float parts[H > 1 ? H : 1][BM];
+    const auto add_missing = [&](bool to_mine) __attribute__((always_inline)) {
+        const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(missing), __float_as_uint(missing), false, false);
+        float sum = __uint_as_float(both[0]) + __uint_as_float(both[1]);
+        if constexpr (H > 1) {
+            if (lane < 32) parts[turn][wave * 32 + lane] = sum;
+            __syncthreads();
+            sum = 0.0f;
+#pragma unroll
+            for (int g = 0; g < H; ++g) sum += parts[g][wave * 32 + (lane & 31)];
+        }
+        if (to_mine) delta += sum;
+        missing = 0.0f;
+    };
+    bool left_out = false;
+    const auto at_edge = [&](int p) { return p < sight.full_from || p + 31 > sight.full_to; };
+    const auto mine_at_edge = [&](int p) { return (p - low) / 32 % H == turn && at_edge(p); };
+    const auto take = [&](int p, unsigned kt, unsigned vt) __attribute__((always_inline)) {
+        const bool edge = at_edge(p);
+        f32x16 x[1];
+        ds_of(x, p, kt, vt, mine, edge);
         bf16x8 w[2];
         to_operands<1>(w, x);
         bf16x8 rest[2];
@@ -110,15 +145,36 @@ __global__ __launch_bounds__(64 * RW * H, RW * H <= 4 && D <= 128 ? 2 : 1) void 
     arrived(q);
     arrived(d_o);
     asm volatile("" : "+v"(lse), "+v"(delta));
-    if (low <= high) issue(low, 0);
-    int set = 0;
-    for (int p = low; p <= high; p += BN, set ^= 1) {
+    // The tiles from `from` to `last`, by the waves whose rows see some of them.
+    const auto over_tiles = [&](int from, int last, const WaveSight& s, auto f) __attribute__((always_inline)) {
+        int set = 0;
+        for (int p = from; p <= last; p += BN, set ^= 1) {
+            wait_loads();
+            __syncthreads();   // every wave's loads of this tile have landed, and its reads of the other set are done
+            if (p + BN <= last) issue(p + BN, set ^ 1, last);
+            for (int u = 32 * turn; u < BN; u += 32 * H)
+                if (s.any && p + u + 32 > s.low && p + u <= s.high)
+                    f(p + u, lds + set * TILE + u * R::BYTES, lds + (2 + set) * TILE + u * R::BYTES);
+        }
+    };
+    bool loaded = false;
+    if (few_keys.first <= few_keys.last) {
+        issue(few_keys.first, 0, few_keys.last);
+        over_tiles(few_keys.first, few_keys.last, few_sight, [&](int p, unsigned kt, unsigned vt) __attribute__((always_inline)) {
+            f32x16 x[1];
+            ds_of(x, p, kt, vt, few, p < few_sight.full_from || p + 31 > few_sight.full_to);
+        });
+        add_missing(is_few);
         wait_loads();
-        __syncthreads();   // every wave's loads of this tile have landed, and its reads of the other set are done
-        if (p + BN <= high) issue(p + BN, set ^ 1);
-        for (int u = 32 * turn; u < BN; u += 32 * H)
-            if (sight.any && p + u + 32 > sight.low && p + u <= sight.high)
-                take(p + u, lds + set * TILE + u * R::BYTES, lds + (2 + set) * TILE + u * R::BYTES);
+        __syncthreads();   // the tiles are read
+        loaded = few_keys.first == low && few_keys.last == high && high - low < BN;   // the only tile is there already
+    }
+    if (low <= high && !loaded) issue(low, 0, high);
+    over_tiles(low, high, sight, take);
+    add_missing(there);
+    if (row < a.T && lane < 32 && turn == 0) {
+        a.stats[stat] = lse;
+        a.stats[(int64_t)a.H * a.T * a.batch + stat] = delta;
     }
 
     // a logit of -infinity has a ds of 0, and 0 times an infinity is NaN

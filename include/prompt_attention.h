@@ -31,7 +31,8 @@
  *
  * Numerics. Products of bf16 numbers are exact, their sums, the softmax and its statistics fp32; the
  * probabilities are rounded to bf16 for their products with v and do, ds to the sum of two bf16
- * numbers for those with k and q; each output is rounded once. Logits are fp32: x_ij log2(e) stays below 2^127. A NaN or an
+ * numbers for those with k and q; each output is rounded once. D_i is summed as p_ij dp_ij, not from
+ * the rounded o, for dk, and for the dq_i of tokens that see at most 128. Logits are fp32: x_ij log2(e) stays below 2^127. A NaN or an
  * infinity reaches the tokens that the formulas lead it to, and no token that does not see it.
  * Results do not depend on timing: no atomics in global memory.
  *
