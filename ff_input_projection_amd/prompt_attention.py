@@ -163,18 +163,19 @@ class PromptAttention:
                 out = tuple(torch.empty(s, dtype=torch.bfloat16, device=dev) for s in self._shapes)
             if workspace is None:
                 workspace = torch.empty((self._workspace_bytes,), dtype=torch.uint8, device=dev)
-        for name, t, shape in zip(("dq", "dk", "dv"), out, self._shapes):
+        dq, dk, dv = out
+        for name, t, shape in zip(("dq", "dk", "dv"), (dq, dk, dv), self._shapes):
             self._check(name, t, shape, dev)
         if workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {dev}")
         st = stream if stream is not None else torch.cuda.current_stream(dev)
         rc = self._lib.prompt_attention_backward(self._h, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                                  None if extents is None else extents.data_ptr(), o.data_ptr(),
-                                                 lse.data_ptr(), do.data_ptr(), *(t.data_ptr() for t in out), workspace.data_ptr(),
-                                                 workspace.numel() * workspace.element_size(), st.cuda_stream)
+                                                 lse.data_ptr(), do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), st.cuda_stream)
         if rc != OK:
             raise FusedProjError(rc, "prompt_attention_backward")
-        return tuple(out)
+        return dq, dk, dv
 
     def close(self):
         if getattr(self, "_h", None) is not None and self._h.value:

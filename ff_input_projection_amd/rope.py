@@ -91,6 +91,8 @@ class Rope:
         if out is None:
             with _allocate_on(stream):
                 out = tuple(torch.empty(s, dtype=self.dtype, device=dev) for s in shapes)
+        if len(out) != len(shapes):
+            raise ValueError(f"{len(out)} outputs are given, {len(shapes)} are wanted")
         for t, shape in zip(out, shapes):
             self._check("an output", t, shape, dev)
         st = stream if stream is not None else torch.cuda.current_stream(dev)
