@@ -259,6 +259,9 @@ struct TileLoads {
 // All outstanding loads of this wave have landed, and its reads of LDS are done (a workgroup of one wave has no
 // barrier that waits for them).
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+// This wave's writes to LDS are done, before direct-to-LDS loads to the same place, which come by another path. The barrier behind
+// it does not see to that in a workgroup of one wave, where it is none.
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 // 32 rows of a wave as operand B of X: row lane % 32 of `src` rows (64-bit address of the lane's
 // row), elements 16 kk + 8 (lane / 32) .. + 7; zeros behind hd and for rows that are not there.

@@ -127,7 +127,10 @@ __global__ __launch_bounds__(64 * RW * H, RW * H <= 4 && D <= 128 ? 2 : 1) void 
         left_out |= add_turned<D, NB, D / 32>(o, w, vt + turned, edge);
     };
 
-    if constexpr (PADDED) __syncthreads();
+    if constexpr (PADDED) {
+        wait_lds();
+        __syncthreads();
+    }
     arrived(q);
     if (low <= high) issue(low, 0);
     int set = 0;

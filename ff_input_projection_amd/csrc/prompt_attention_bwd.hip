@@ -141,7 +141,10 @@ __global__ __launch_bounds__(64 * RW * H, RW * H <= 4 && D <= 128 ? 2 : 1) void 
         left_out |= add_turned<D, 1, D / 32>(dq, w, kt + turned, edge, rest);
     };
 
-    if constexpr (PADDED) __syncthreads();
+    if constexpr (PADDED) {
+        wait_lds();
+        __syncthreads();
+    }
     arrived(q);
     arrived(d_o);
     asm volatile("" : "+v"(lse), "+v"(delta));
@@ -303,7 +306,10 @@ __global__ __launch_bounds__(64 * RW * H * PARTS, RW * H * PARTS <= 4 && D <= 96
         add_turned<D, 1, C, PARTS>(dk, dw, qt + turned, edge, rest);
     };
 
-    if constexpr (PADDED) __syncthreads();
+    if constexpr (PADDED) {
+        wait_lds();
+        __syncthreads();
+    }
     arrived(k);
     if constexpr (!V_IN_LDS) arrived(v);
     int set = 0;
