@@ -51,15 +51,16 @@ struct AttentionPlan {
 //   64 x 512 (256)                          13 / 13, 18 / 24      16 x 2048, causal (256)  38 / 29, 52 / 38
 //   128 x 512 (512)                         17 / 22, 30 / 47      16 x 4096, causal (512)  89 / 65, 132 / 121
 //   32 x 2048 (512)                         51 / 59, 83 / 114     64 x 2048, causal (1024) 74 / 75, 122 / 141
-// Up to 128 tokens there are one or two tiles of keys, and nothing to share. Large groups gain less
-// (32 heads on 8 of 128 x 2048, causal, 512: 57 / 71).
+// Up to 128 tokens there are one or two tiles of keys, and nothing to share. Large groups gain less: 32 heads on 8 of 128 x 2048,
+// causal (512) take 57 / 71, so the border for causal heads of 128 is drawn between them and 16 ungrouped heads x 4096, which
+// lose by it (132 / 121).
 inline bool few_workgroups(int64_t blocks, const prompt_attention_desc& d) {
     return d.tokens > 128 && (blocks < 256 || (d.tokens >= 1024 && blocks < (d.causal && d.head_dim <= 64 ? 768 : 512)));
 }
 
 // Sequences of up to 64 tokens: workgroups with a row of waves for every 32 that there are, and none idle. Forward and
-// backward, us, 128 tokens a workgroup / these: 512 x 32 tokens, 32 heads on 8 of 128, causal, 157, 395 / 95, 247; 512 x 17, 12
-// of 64, 24, 72 / 15, 36; 256 x 64, 32 on 8 of 128, 98, 279 / 85, 262. One sequence of 64 has no gain (backward 25 / 32).
+// backward, us, 128 tokens a workgroup / these: 512 x 32 tokens, 32 heads on 8 of 128, causal, 156, 439 / 95, 260; 512 x 17, 12
+// of 64, 24, 83 / 14, 40; 256 x 64, 32 on 8 of 128, 96, 304 / 83, 277. One sequence of 64 has no gain (backward 26 / 34).
 inline int short_rows(const prompt_attention_desc& d) {   // 0: the sequences are not short
     if (d.tokens <= 32) return 1;
     return d.tokens <= 64 && d.batch * d.n_heads >= 512 ? 2 : 0;
@@ -291,7 +292,9 @@ __device__ __forceinline__ void arrived(bf16x8 (&x)[N]) {
 // The rows of a lane's 16 values of a 32 x 32 product.
 __device__ __forceinline__ int value_row(int i) { return (i & 3) + 8 * (i >> 2) + 4 * ((threadIdx.x & 63) >> 5); }
 
-// X, rounded, as operands B of Y^T.
+// X, rounded, as operands B of Y^T. Probabilities are one bf16 number: o and dv are off by 0.0023 of their norm then, of which 0.0017 is
+// their own rounding. As two numbers, a product more, they would be off by that alone, and 8192 tokens, 32 heads on 8 of 128, causal,
+// would take 762 us for 573, forward and backward of 2 x 4096 1746 for 1553, of a ragged batch of 32 x 512, 12 of 64, 160 for 145.
 template <int NB>
 __device__ __forceinline__ void to_operands(bf16x8 (&o)[2 * NB], const f32x16 (&x)[NB]) {
 #pragma unroll

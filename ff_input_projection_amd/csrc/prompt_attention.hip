@@ -12,10 +12,11 @@
 // tokens and take 32 keys of 128 each (few_workgroups has both sides' times); above heads of 128 the
 // registers hold one wave a SIMD and tiles of 32. Short sequences have workgroups without idle waves (short_rows). k and v come by direct-to-LDS loads, two tiles each.
 //
-// Measured: 8192 tokens, 32 heads on 8 of 128, causal, 555 us: 990 TFLOP/s, 0.8 of a large
+// Measured: 8192 tokens, 32 heads on 8 of 128, causal, 549 to 585 us on different cards (power): 940 to 1000 TFLOP/s, 0.8 of a large
 // library product's rate. Bound by both units of a SIMD: matrix units busy 4/10 of the time, vector
-// units half. Without the softmax's operations it takes 504 us, without the second product 408, on zeros 473 (the clock:
-// power).
+// units half. At a step that took 575 us it was 504 without the softmax's operations, 408 without the second product, and 473 instead of 598
+// on zeros (another card; the clock: power). Heads of 64 have half the products a logit: 2 x 4096 tokens, 5 heads, all see all, 77 us,
+// vector units busy half of the time and matrix units a fifth, and 1.25 rounds of workgroups, so that a CU has none for a quarter of it.
 #include <cmath>
 #include <cstring>
 #include <new>

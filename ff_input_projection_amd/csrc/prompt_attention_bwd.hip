@@ -4,7 +4,7 @@
 // Two kernels, both with the logits computed again. The first passes over the keys like the
 // forward pass, for 128 tokens of a query head, and leaves dq; it also leaves D and lse log2(e) of its
 // tokens for the second. The second passes over the tokens that see 128 keys, head after head of
-// the group, and leaves dk and dv. 7 products of the forward pass's size where 5 would do in one
+// the group, and leaves dk and dv. 9 products, 4 and 5 (those with ds count twice, as it is two numbers), where 7 would do in one
 // kernel: there dq would be summed by atomics, in an order that changes from run to run, or
 // through partial sums in memory.
 //
@@ -21,9 +21,10 @@ using namespace fp::dev;
 using fp::AttentionArgs;
 
 // Rows that see at most this many keys have their D corrected before dq is formed, by two products more for these keys. In other
-// rows what o's rounding leaves in dq falls with the root of the number of keys that their softmax spreads over: normal inputs,
-// 512 tokens, causal, dq is off by 0.0020 of its norm without any of it, by 0.0017 with; with logits three times as steep by
-// 0.0030 and 0.0025, and by 0.0017 if all rows were. The backward pass in us, none / these / all rows: 2 x 4096 tokens, 32 heads on 8 of 128,
+// rows what o's rounding leaves in dq falls with the root of the number of keys that their softmax spreads over, but for what these keys
+// have in common. 512 tokens, causal, normal inputs: dq is off by 0.0020 of its norm without any of it, by 0.0017 with; logits three times as
+// steep, 0.0030 and 0.0025; 32 x 512 ragged, all see all, keys with a common part, 0.0022 and 0.0022; 0.0017 if all rows were corrected. The
+// backward pass in us, none / these / all rows: 2 x 4096 tokens, 32 heads on 8 of 128,
 // causal, 1522 / 1526 / 1788; 32 x 512 ragged, 12 of 64, 145 / 145 / 164; 256 x 128, 32 on 8 of 128, 532 / 582 / 582; 512 x 7, 176 / 191 / 191.
 constexpr int kFewKeys = 128;
 
@@ -375,11 +376,11 @@ __global__ __launch_bounds__(64 * RW * H * PARTS, RW * H * PARTS <= 4 && D <= 96
 
 // Workgroups of 128 keys are few for longer than those of tokens: a group's heads are in one, and with a causal mask the first
 // has twice the mean's work. dq and dk, dv, heads of 64, us, with 4 rows of one wave / 4 of 2 / 2 of 4 (dq as it is best):
-//   4 x 512 tokens, 12 heads (192 workgroups)    - / 36 / 41        8 x 512, 12 heads (384)  46 / 52 / -
-//   16 x 2048 (256)     108 / 94 / 100           causal             108 / 78 / 66
-//   32 x 2048 (512)     147 / 157 / 174          causal             133 / 136 / 129       16 x 4096, causal  236 / 194 / 205
-// (All with ds in one bf16 number; 2 x 4096 tokens, 32 heads on 8 of 128, causal, take a seventh longer with two.) Heads of 128 have registers for one wave a SIMD
-// of 4 rows of one, and take two.
+//   4 x 512 tokens, 12 heads (192 workgroups)  47 / 45 / 49         8 x 512, 12 heads (384)  59 / 67 / 67     16 x 512 (768)  90 / 101 / 111
+//   16 x 2048 (256)     135 / 117 / 119          causal             106 / 92 / 75
+//   32 x 2048 (512)     193 / 200 / 210          causal             161 / 164 / 146       16 x 4096, causal (512)  282 / 233 / 238
+// and heads of 128, which have registers for one wave a SIMD of 4 rows of one, causal:
+//   16 x 2048 (256)     163 / 134 / 116          16 x 4096 (512)    459 / 409 / 425       32 x 2048 (512)  303 / 256 / 235
 int64_t few_key_blocks(const prompt_attention_desc& d) { return d.tokens < 1024 ? 160 : d.causal ? 512 : 256; }
 
 // Adds up the parts of dk and dv, 4 elements a thread.
@@ -460,8 +461,9 @@ namespace fp {
 
 void plan_attention_backward(const prompt_attention_desc& d, int64_t kvh, AttentionPlan* p) {
     // Where the workgroups are of 64 keys and still fewer than twice the CUs (one is on a CU at a time), a group's heads are cut into parts;
-    // their sums go through memory. The whole backward pass, causal, without and with parts: 32 heads on 8 of 128, 512 tokens 60 and 44 us,
-    // 2048 tokens 222 and 182; 16 on 4 of 256, 1024 tokens 352 and 155.
+    // their sums go through memory. The whole backward pass, causal, without and with parts: 32 heads on 8 of 128, 512 tokens 67 and 47 us,
+    // 2048 tokens 253 and 209; 16 on 4 of 256, 1024 tokens 389 and 168. Parts are of whole heads, the number of a part rounded up, so there may be
+    // fewer workgroups than wanted (2999 tokens, 16 heads on 4: 376).
     const int64_t group = d.n_heads / kvh, blocks = d.batch * kvh * ((d.tokens + 63) / 64);
     const bool small = p->dim > 128 || d.batch * kvh * ((d.tokens + 127) / 128) < few_key_blocks(d);
     p->kv_parts = 1;

@@ -42,7 +42,8 @@ class Rope:
     head-major q and k, in place with ``out=(q, k)``; ``rotate_backward(dq, dk, positions)`` is
     its backward pass. Outputs may be passed in; launches go to torch's current stream (or
     ``stream``) and are asynchronous. A plan belongs to the device that was current when it was
-    made: its tensors are on that device, and it is the current one in every call.
+    made: its tensors are on that device, and it is the current one in every call. It holds the pairs'
+    angles in device memory, so keep it as long as a graph that captured its calls is replayed.
     """
 
     def __init__(self, batch: int, tokens: int, n_heads: int, head_dim: int, **kw):

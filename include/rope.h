@@ -32,7 +32,8 @@
  * contents at replay) may hold any number, below 0 too; NULL stands for 0 .. T - 1.
  *
  * Memory: the caller owns every device buffer; the plan owns its table of pairs and is only
- * read by calls, so it may be used from several host threads and streams at once. Errors are
+ * read by calls, so it may be used from several host threads and streams at once. It has to
+ * outlive the replays of graphs that captured them. Errors are
  * the FUSED_PROJ_* codes; fused_proj_strerror() describes them.
  */
 #ifndef ROPE_H
