@@ -23,9 +23,9 @@ using fp::AttentionArgs;
 // Rows that see at most this many keys have their D corrected before dq is formed, by two products more for these keys. In other
 // rows what o's rounding leaves in dq falls with the root of the number of keys that their softmax spreads over, but for what these keys
 // have in common. 512 tokens, causal, normal inputs: dq is off by 0.0020 of its norm without any of it, by 0.0017 with; logits three times as
-// steep, 0.0030 and 0.0025; 32 x 512 ragged, all see all, keys with a common part, 0.0022 and 0.0022; 0.0017 if all rows were corrected. The
-// backward pass in us, none / these / all rows: 2 x 4096 tokens, 32 heads on 8 of 128,
-// causal, 1522 / 1526 / 1788; 32 x 512 ragged, 12 of 64, 145 / 145 / 164; 256 x 128, 32 on 8 of 128, 532 / 582 / 582; 512 x 7, 176 / 191 / 191.
+// steep, 0.0030 and 0.0025; 32 x 512 ragged, all see all, keys with a common part, 0.0022 and 0.0022; 0.0017 if all rows were corrected. Times,
+// us, none / these / all rows: forward and backward of 2 x 4096 tokens, 32 heads on 8 of 128, causal, 1522 / 1526 / 1788, of 32 x 512 ragged,
+// 12 of 64, 145 / 145 / 164; backward of 256 x 128, 32 on 8 of 128, causal, 532 / 582 / 582, of 512 x 7, 176 / 191 / 191.
 constexpr int kFewKeys = 128;
 
 // Shapes of a workgroup: RW rows of waves with 32 tokens each, and H waves a row that share them and take S
